@@ -18,7 +18,9 @@ KOSMOS_MAX_P = 8
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE = range(7)
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "WORKSPACE", 4: "CUDA", 5: "TIMEOUT",
                 6: "DEVICE"}
-BF16, MXFP8_E4M3 = 0, 1
+BF16, MXFP8_E4M3, FP16, FP32 = 0, 1, 2, 3
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ROUTE_MAX_EXPERTS, ROUTE_MAX_TOPK, ROUTE_MAX_GROUPS = 1024, 16, 32
 OP_AG_GEMM, OP_GEMM_RS, OP_MOE_FWD = 0, 1, 2
 SCHED_SELF, SCHED_FIXED, SCHED_UNFUSED = 0, 1, 2
 ORDER_BAND, ORDER_ROW = 0, 1
@@ -38,7 +40,8 @@ EXPORTS = ["kosmos_default_opts", "kosmos_num_sms", "kosmos_workspace_bytes", "k
            "kosmos_trace_info", "kosmos_rail_decode", "kosmos_rail_decode_device", "kosmos_ag_gemm_noalloc",
            "kosmos_moe_workspace_bytes", "kosmos_moe_debug_view", "kosmos_ag_tile_plan", "kosmos_moe_bwd",
            "kosmos_moe_bwd_workspace_bytes", "kosmos_moe_bwd_debug_view", "kosmos_ag_gemm_host",
-           "kosmos_noalloc_status_sync"]
+           "kosmos_noalloc_status_sync", "kosmos_default_router", "kosmos_route", "kosmos_route_workspace_bytes",
+           "kosmos_route_bwd", "kosmos_grad_norm", "kosmos_grad_clip", "kosmos_grad_workspace_bytes"]
 
 
 class KosmosError(RuntimeError):
@@ -55,6 +58,12 @@ class Opts(C.Structure):
                 ("cta_pair", C.c_int32), ("plain_launch", C.c_int32),
                 ("wait_limit_ns", C.c_uint64), ("inject", C.c_uint64), ("tail_split", C.c_int64),
                 ("link_gbs", C.c_int64)]
+
+
+class Router(C.Structure):
+    """What a router does (kosmos_router): score, topk, groups, renorm, scale."""
+    _fields_ = [("score", C.c_int32), ("topk", C.c_int32), ("n_groups", C.c_int32), ("topk_groups", C.c_int32),
+                ("group_top", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32)]
 
 
 class TraceRec(C.Structure):
@@ -125,6 +134,20 @@ def lib():
     L.kosmos_moe_bwd_debug_view.argtypes = [i32, i32, i64, i64, i32, i32, i64, vp, C.POINTER(vp), C.POINTER(i64)]
     L.kosmos_moe_bwd_debug_view.restype = i32
     L.kosmos_ag_tile_plan.restype = i32
+    L.kosmos_default_router.argtypes = [C.POINTER(Router)]
+    L.kosmos_default_router.restype = None
+    L.kosmos_route.argtypes = [vp, i32, i64, i32, i64, C.POINTER(Router), vp, vp, vp, vp, vp, C.c_size_t, vp]
+    L.kosmos_route.restype = i32
+    L.kosmos_route_workspace_bytes.argtypes = [i32]
+    L.kosmos_route_workspace_bytes.restype = C.c_size_t
+    L.kosmos_route_bwd.argtypes = [vp, i32, i64, i32, i64, C.POINTER(Router), vp, vp, vp, vp, i64, vp]
+    L.kosmos_route_bwd.restype = i32
+    L.kosmos_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, vp, C.c_size_t, vp]
+    L.kosmos_grad_norm.restype = i32
+    L.kosmos_grad_clip.argtypes = [vp, vp, vp, vp, i32, C.c_float, vp, vp, C.c_size_t, vp]
+    L.kosmos_grad_clip.restype = i32
+    L.kosmos_grad_workspace_bytes.argtypes = [vp, vp, i32]
+    L.kosmos_grad_workspace_bytes.restype = C.c_size_t
     _lib = L
     return L
 
@@ -349,6 +372,157 @@ def moe_bwd_debug_view(what: int, P: int, tokens: int, hidden: int, n_experts: i
                                            C.byref(ptr), C.byref(nb)), "kosmos_moe_bwd_debug_view")
     off = ptr.value - ws.data_ptr()
     return ws[off:off + nb.value]
+
+
+def router(topk: int, score: int = SCORE_SOFTMAX, n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+           renorm: bool = True, scale: float = 1.0) -> Router:
+    """A router's description for route and route_bwd."""
+    r = Router()
+    lib().kosmos_default_router(C.byref(r))
+    r.score, r.topk, r.n_groups, r.topk_groups, r.group_top = score, topk, n_groups, topk_groups, group_top
+    r.renorm, r.scale = int(bool(renorm)), scale
+    return r
+
+
+def _plain_dtype(t) -> int:
+    import torch
+    d = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(t.dtype)
+    if d is None:
+        raise ValueError(f"kosmos: bf16, fp16 or fp32 expected, not {t.dtype}")
+    return d
+
+
+def _check_like(what: str, t, dtype, shape):
+    """t (or None): a contiguous CUDA tensor of this type and shape."""
+    if t is None:
+        return
+    if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} and shape {tuple(shape)} expected, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def _check_rows(what: str, t):
+    """t: a CUDA matrix whose rows are contiguous (any row stride)."""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a CUDA matrix with contiguous rows expected")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{what}: rows overlap (row stride {t.stride(0)} < {t.shape[1]} columns)")
+
+
+def _ld(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def route_workspace(n_experts: int, device=None):
+    """A zeroed workspace tensor (uint8) for route with expert_counts."""
+    import torch
+    nbytes = int(lib().kosmos_route_workspace_bytes(n_experts))
+    if nbytes == 0:
+        raise KosmosError(ERR_INVALID_ARG, "kosmos_route_workspace_bytes")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def route(logits, r: Router, topk_idx, topk_gate, bias=None, expert_counts=None, ws=None, stream=None):
+    """The topk experts (topk_idx, int32) and gates (topk_gate, fp32) of every
+    token: logits [tokens, experts] in bf16, fp16 or fp32, with any row
+    stride.  bias [experts] fp32 takes part in the choice only.
+    expert_counts [experts] int32 receives the tokens per expert and needs
+    ws = route_workspace(experts)."""
+    import torch
+    _check_rows("route: logits", logits)
+    T, E = logits.shape
+    _check_like("route: topk_idx", topk_idx, torch.int32, (T, r.topk))
+    _check_like("route: topk_gate", topk_gate, torch.float32, (T, r.topk))
+    _check_like("route: bias", bias, torch.float32, (E,))
+    _check_like("route: expert_counts", expert_counts, torch.int32, (E,))
+    _check_cuda(ws)
+    rc = lib().kosmos_route(logits.data_ptr(), _plain_dtype(logits), T, E, _ld(logits), C.byref(r),
+                            bias.data_ptr() if bias is not None else None, topk_idx.data_ptr(), topk_gate.data_ptr(),
+                            expert_counts.data_ptr() if expert_counts is not None else None,
+                            ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                            _stream(stream))
+    _raise(rc, "kosmos_route")
+
+
+def route_bwd(logits, r: Router, topk_idx, topk_gate, dgate, dlogits, stream=None):
+    """dlogits (the logits' type) from dgate: the gradient of route's gates
+    with the choice of experts held fixed."""
+    import torch
+    _check_rows("route_bwd: logits", logits)
+    _check_rows("route_bwd: dlogits", dlogits)
+    T, E = logits.shape
+    if dlogits.dtype != logits.dtype or tuple(dlogits.shape) != (T, E):
+        raise ValueError("route_bwd: dlogits needs the logits' type and shape")
+    _check_like("route_bwd: topk_idx", topk_idx, torch.int32, (T, r.topk))
+    _check_like("route_bwd: topk_gate", topk_gate, torch.float32, (T, r.topk))
+    _check_like("route_bwd: dgate", dgate, torch.float32, (T, r.topk))
+    rc = lib().kosmos_route_bwd(logits.data_ptr(), _plain_dtype(logits), T, E, _ld(logits), C.byref(r),
+                                topk_idx.data_ptr(), topk_gate.data_ptr(), dgate.data_ptr(), dlogits.data_ptr(),
+                                _ld(dlogits), _stream(stream))
+    _raise(rc, "kosmos_route_bwd")
+
+
+class GradSet:
+    """A list of gradient tensors (bf16, fp16, fp32; contiguous CUDA tensors of
+    any size and alignment) marshalled once for grad_norm and grad_clip, and
+    the tensors that grad_clip writes (outs; the gradients themselves if not
+    given).  It keeps the tensors alive and reads them anew in every call."""
+
+    def __init__(self, grads: Sequence, outs: Optional[Sequence] = None):
+        self.grads = list(grads)
+        self.outs = list(outs) if outs is not None else self.grads
+        if len(self.outs) != len(self.grads):
+            raise ValueError("GradSet: one output per gradient expected")
+        _check_cuda(*self.grads, *self.outs)
+        for g, o in zip(self.grads, self.outs):
+            if g.dtype != o.dtype or g.numel() != o.numel():
+                raise ValueError("GradSet: an output differs from its gradient in type or size")
+        self.n = len(self.grads)
+        self.ptrs = _ptrs(self.grads)
+        self.out_ptrs = _ptrs(self.outs)
+        self.sizes = (C.c_int64 * self.n)(*[t.numel() for t in self.grads])
+        self.dtypes = (C.c_int32 * self.n)(*[_plain_dtype(t) for t in self.grads])
+
+
+def _grad_set(grads) -> GradSet:
+    return grads if isinstance(grads, GradSet) else GradSet(grads)
+
+
+def grad_workspace(grads, device=None):
+    """A zeroed workspace tensor (uint8) for grad_norm / grad_clip of this set."""
+    import torch
+    s = _grad_set(grads)
+    nbytes = int(lib().kosmos_grad_workspace_bytes(s.sizes, s.dtypes, s.n))
+    if nbytes == 0:
+        raise KosmosError(ERR_INVALID_ARG, "kosmos_grad_workspace_bytes")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def grad_norm(grads, norm, ws, tensor_norms=None, stream=None):
+    """norm (fp32, one element) = the 2-norm of all gradients together (a
+    GradSet or a list of tensors); tensor_norms (fp32, one per tensor) = the
+    norm of each."""
+    import torch
+    s = _grad_set(grads)
+    _check_like("grad_norm: norm", norm, torch.float32, (1,))
+    _check_like("grad_norm: tensor_norms", tensor_norms, torch.float32, (s.n,))
+    _check_cuda(ws)
+    rc = lib().kosmos_grad_norm(s.ptrs, s.sizes, s.dtypes, s.n, norm.data_ptr(),
+                                tensor_norms.data_ptr() if tensor_norms is not None else None, ws.data_ptr(),
+                                ws.numel(), _stream(stream))
+    _raise(rc, "kosmos_grad_norm")
+
+
+def grad_clip(grads, max_norm: float, norm, ws, stream=None):
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or
+    into the GradSet's outs; norm (fp32, one element) receives the norm."""
+    import torch
+    s = _grad_set(grads)
+    _check_like("grad_clip: norm", norm, torch.float32, (1,))
+    _check_cuda(ws)
+    rc = lib().kosmos_grad_clip(s.ptrs, s.out_ptrs, s.sizes, s.dtypes, s.n, max_norm, norm.data_ptr(), ws.data_ptr(),
+                                ws.numel(), _stream(stream))
+    _raise(rc, "kosmos_grad_clip")
 
 
 def mxfp8_scale_bytes(rows: int, cols: int, along_cols: bool) -> int:

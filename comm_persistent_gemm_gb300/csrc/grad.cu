@@ -1,0 +1,246 @@
+// grad.cu -- the global norm of many gradient tensors, and clipping by it.
+//
+// The tensors' descriptors travel as a kernel parameter (up to GRAD_MAX_T per
+// launch; a longer list takes several launches on the stream), so a call needs
+// no table in device memory and can be captured into a graph.  Every tensor is
+// cut into chunks; one block sums one chunk at a time, and the last block of a
+// launch adds the chunks' sums up in their order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace kosmos {
+
+namespace {
+
+constexpr int GRAD_THREADS = 256;
+constexpr int GRAD_MAX_T = 1000;             // descriptors of one launch: 32,000 bytes of kernel parameter
+constexpr int64_t GRAD_MIN_CHUNK = 16384;    // bytes: one pass of a block's 16-byte loads, four per thread
+constexpr int64_t GRAD_CHUNKS = 9728;        // chunks of a large set
+
+struct GradTensor {
+    const void *x;
+    void *out;
+    int64_t n;        // elements
+    int32_t chunk0;   // this tensor's first chunk within the launch
+    int32_t dtype;
+};
+
+// Workspace: the 256-byte header (its done_ctas counts finished blocks), then
+// this, then one fp64 sum per chunk of a launch.
+struct GradScratch {
+    double total;     // sum of squares of the launches so far
+    float coef;       // the clip factor
+};
+
+template <int N> struct GradParams {
+    WsHeader *hdr;
+    GradScratch *scr;
+    double *part;
+    float *norm, *tensor_norms;   // tensor_norms: of this launch's first tensor
+    int64_t chunk_bytes;
+    int nt, chunks;
+    int first, last;              // the launch begins / ends the set
+    float max_norm;
+    GradTensor t[N];
+};
+
+__device__ __forceinline__ float elem(const float *p) { return *p; }
+__device__ __forceinline__ float elem(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float elem(const __half *p) { return __half2float(*p); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
+
+// The last tensor whose first chunk is not after chunk c (empty tensors share
+// their successor's first chunk and are passed over).
+template <int N> __device__ __forceinline__ int tensor_of(const GradParams<N> &p, int c) {
+    int lo = 0, hi = p.nt - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.t[mid].chunk0 <= c) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// A block's fp64 sum, in a fixed order; valid in thread 0.
+__device__ __forceinline__ double block_sum(double v, double *s_red) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double r = 0.0;
+    if (threadIdx.x == 0)
+        for (int i = 0; i < GRAD_THREADS / 32; ++i) r += s_red[i];
+    __syncthreads();
+    return r;
+}
+
+template <typename T> __device__ __forceinline__ double chunk_squares(const T *x, int64_t e0, int64_t e1) {
+    double acc = 0.0;
+    for (int64_t i = e0 + threadIdx.x; i < e1; i += GRAD_THREADS) {
+        const double v = elem(x + i);
+        acc += v * v;
+    }
+    return acc;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T *x, T *out, int64_t e0, int64_t e1, float coef) {
+    for (int64_t i = e0 + threadIdx.x; i < e1; i += GRAD_THREADS) put(out + i, elem(x + i) * coef);
+}
+
+template <int N> __device__ __forceinline__ void chunk_range(const GradParams<N> &p, int i, int c, int64_t &e0,
+                                                             int64_t &e1) {
+    const int64_t per = p.chunk_bytes / (p.t[i].dtype == KOSMOS_FP32 ? 4 : 2);
+    e0 = (c - p.t[i].chunk0) * per;
+    e1 = e0 + per < p.t[i].n ? e0 + per : p.t[i].n;
+}
+
+template <int N>
+__global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const __grid_constant__ GradParams<N> p) {
+    __shared__ double s_red[GRAD_THREADS / 32];
+    __shared__ double s_sum[N];
+    __shared__ int s_last;
+    for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+        const int i = tensor_of(p, c);
+        int64_t e0, e1;
+        chunk_range(p, i, c, e0, e1);
+        double v;
+        if (p.t[i].dtype == KOSMOS_BF16) v = chunk_squares(static_cast<const __nv_bfloat16 *>(p.t[i].x), e0, e1);
+        else if (p.t[i].dtype == KOSMOS_FP16) v = chunk_squares(static_cast<const __half *>(p.t[i].x), e0, e1);
+        else v = chunk_squares(static_cast<const float *>(p.t[i].x), e0, e1);
+        v = block_sum(v, s_red);
+        if (threadIdx.x == 0) p.part[c] = v;
+    }
+    // the last block joins the chunks, tensor by tensor, in their order
+    if (threadIdx.x == 0) {
+        __threadfence();
+        s_last = atomicAdd(&p.hdr->done_ctas, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < p.nt; i += GRAD_THREADS / 32) {
+        const int c1 = i + 1 < p.nt ? p.t[i + 1].chunk0 : p.chunks;
+        double v = 0.0;
+        for (int c = p.t[i].chunk0 + lane; c < c1; c += 32) v += __ldcg(&p.part[c]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+        if (lane == 0) {
+            s_sum[i] = v;
+            if (p.tensor_norms != nullptr) p.tensor_norms[i] = static_cast<float>(sqrt(v));
+        }
+    }
+    __syncthreads();
+    double v = 0.0;
+    for (int i = threadIdx.x; i < p.nt; i += GRAD_THREADS) v += s_sum[i];
+    v = block_sum(v, s_red);
+    if (threadIdx.x == 0) {
+        if (!p.first) v += p.scr->total;
+        p.scr->total = v;
+        if (p.last) {
+            const double norm = sqrt(v);
+            p.norm[0] = static_cast<float>(norm);
+            const double f = static_cast<double>(p.max_norm) / (norm + 1e-6);
+            p.scr->coef = f > 1.0 ? 1.0f : static_cast<float>(f);  // a NaN stays a NaN
+        }
+        p.hdr->done_ctas = 0u;
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(GRAD_THREADS) grad_scale_kernel(const __grid_constant__ GradParams<N> p) {
+    const float coef = p.scr->coef;
+    for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+        const int i = tensor_of(p, c);
+        if (coef == 1.0f && p.t[i].out == p.t[i].x) continue;
+        int64_t e0, e1;
+        chunk_range(p, i, c, e0, e1);
+        if (p.t[i].dtype == KOSMOS_BF16)
+            chunk_scale(static_cast<const __nv_bfloat16 *>(p.t[i].x), static_cast<__nv_bfloat16 *>(p.t[i].out), e0, e1, coef);
+        else if (p.t[i].dtype == KOSMOS_FP16)
+            chunk_scale(static_cast<const __half *>(p.t[i].x), static_cast<__half *>(p.t[i].out), e0, e1, coef);
+        else
+            chunk_scale(static_cast<const float *>(p.t[i].x), static_cast<float *>(p.t[i].out), e0, e1, coef);
+    }
+}
+
+int elem_bytes(int dtype) { return dtype == KOSMOS_FP32 ? 4 : 2; }
+
+// Chunks are large enough that a large set has about GRAD_CHUNKS of them
+// (64 per SM: the uneven end of a pass stays under 2 %), and at least one
+// pass of a block, so that a small set still spreads over the SMs.
+int64_t grad_chunk_bytes(const int64_t *sizes, const int32_t *dtypes, int n) {
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) total += sizes[i] * elem_bytes(dtypes[i]);
+    const int64_t c = align_up(cdiv(total, GRAD_CHUNKS), 4096);
+    return c < GRAD_MIN_CHUNK ? GRAD_MIN_CHUNK : c;
+}
+
+template <int N> kosmos_status launch_grad_n(const GradLaunch &L, int64_t chunk_bytes, cudaStream_t stream) {
+    GradParams<N> p;
+    uint8_t *ws = static_cast<uint8_t *>(L.ws);
+    p.hdr = reinterpret_cast<WsHeader *>(ws);
+    p.scr = reinterpret_cast<GradScratch *>(ws + 256);
+    p.part = reinterpret_cast<double *>(ws + 512);
+    p.norm = L.norm;
+    p.chunk_bytes = chunk_bytes;
+    p.max_norm = L.max_norm;
+    for (int pass = 0; pass < (L.outs != nullptr ? 2 : 1); ++pass) {
+        int i0 = 0;
+        do {
+            const int nt = L.n - i0 < N ? L.n - i0 : N;
+            int64_t chunks = 0;
+            for (int i = 0; i < nt; ++i) {
+                GradTensor &t = p.t[i];
+                t.x = L.grads[i0 + i];
+                t.out = L.outs != nullptr ? L.outs[i0 + i] : nullptr;
+                t.n = L.sizes[i0 + i];
+                t.dtype = L.dtypes[i0 + i];
+                t.chunk0 = static_cast<int32_t>(chunks);
+                chunks += cdiv(t.n * elem_bytes(t.dtype), chunk_bytes);
+            }
+            p.nt = nt;
+            p.chunks = static_cast<int>(chunks);
+            p.first = i0 == 0;
+            p.last = i0 + nt >= L.n;
+            p.tensor_norms = L.tensor_norms != nullptr ? L.tensor_norms + i0 : nullptr;
+            int64_t blocks = chunks < 4ll * L.sms ? chunks : 4ll * L.sms;
+            if (blocks < 1) blocks = 1;
+            if (pass == 0)
+                grad_norm_kernel<N><<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, stream>>>(p);
+            else if (chunks > 0)
+                grad_scale_kernel<N><<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, stream>>>(p);
+            if (cudaGetLastError() != cudaSuccess) return KOSMOS_ERR_CUDA;
+            i0 += nt;
+        } while (i0 < L.n);
+    }
+    return KOSMOS_OK;
+}
+
+}  // namespace
+
+size_t grad_workspace_bytes(const int64_t *sizes, const int32_t *dtypes, int n) {
+    const int64_t chunk = grad_chunk_bytes(sizes, dtypes, n);
+    int64_t most = 0, chunks = 0;
+    for (int i = 0; i < n; ++i) {
+        if (i % GRAD_MAX_T == 0) chunks = 0;
+        chunks += cdiv(sizes[i] * elem_bytes(dtypes[i]), chunk);
+        if (chunks > most) most = chunks;
+    }
+    return 512 + static_cast<size_t>(align_up(8 * most, 256));
+}
+
+kosmos_status launch_grad(const GradLaunch &L, cudaStream_t stream) {
+    const int64_t chunk = grad_chunk_bytes(L.sizes, L.dtypes, L.n);
+    if (L.n <= 32) return launch_grad_n<32>(L, chunk, stream);
+    if (L.n <= 256) return launch_grad_n<256>(L, chunk, stream);
+    return launch_grad_n<GRAD_MAX_T>(L, chunk, stream);
+}
+
+}  // namespace kosmos

@@ -764,6 +764,130 @@ kosmos_status kosmos_mxfp8_quantize(const void *x, int64_t rows, int64_t cols, i
     return launch_mxfp8_quantize(x, rows, cols, along_cols, q, scales, static_cast<cudaStream_t>(stream));
 }
 
+void kosmos_default_router(kosmos_router *router) {
+    if (!router) return;
+    memset(router, 0, sizeof(*router));
+    router->score = KOSMOS_SCORE_SOFTMAX;
+    router->topk = 1;
+    router->n_groups = router->topk_groups = router->group_top = 1;
+    router->renorm = 1;
+    router->scale = 1.0f;
+}
+
+// Bytes of an element of the routing and gradient operators' types, 0 otherwise.
+static int plain_dtype_bytes(int dtype) {
+    return dtype == KOSMOS_BF16 || dtype == KOSMOS_FP16 ? 2 : dtype == KOSMOS_FP32 ? 4 : 0;
+}
+
+static bool aligned_to(const void *p, int bytes) {
+    return p != nullptr && reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0;
+}
+
+static bool route_args_ok(int dtype, int64_t tokens, int n_experts, int64_t ld, const kosmos_router *r) {
+    if (r == nullptr || plain_dtype_bytes(dtype) == 0) return false;
+    if (tokens < 0 || tokens > (1ll << 30) || n_experts < 1 || n_experts > KOSMOS_ROUTE_MAX_EXPERTS) return false;
+    if (ld < n_experts || ld > (1ll << 32)) return false;
+    if (r->score != KOSMOS_SCORE_SOFTMAX && r->score != KOSMOS_SCORE_SIGMOID) return false;
+    if (r->n_groups < 1 || r->n_groups > KOSMOS_ROUTE_MAX_GROUPS || n_experts % r->n_groups != 0) return false;
+    if (r->topk_groups < 1 || r->topk_groups > r->n_groups) return false;
+    const int per_group = n_experts / r->n_groups;
+    if (r->group_top < 1 || r->group_top > 2 || (r->n_groups > 1 && r->group_top > per_group)) return false;
+    if (r->topk < 1 || r->topk > KOSMOS_ROUTE_MAX_TOPK || r->topk > r->topk_groups * per_group) return false;
+    return r->scale > 0.0f && r->scale <= 3.402823466e38f;
+}
+
+size_t kosmos_route_workspace_bytes(int n_experts) {
+    if (n_experts < 1 || n_experts > KOSMOS_ROUTE_MAX_EXPERTS) return 0;
+    return route_workspace_bytes(n_experts);
+}
+
+kosmos_status kosmos_route(const void *logits, int dtype, int64_t tokens, int n_experts, int64_t ld_logits,
+                           const kosmos_router *router, const float *bias, int32_t *topk_idx, float *topk_gate,
+                           int32_t *expert_counts, void *ws, size_t ws_bytes, void *stream) {
+    if (!route_args_ok(dtype, tokens, n_experts, ld_logits, router)) return KOSMOS_ERR_INVALID_ARG;
+    if (tokens > 0 && (!aligned_to(logits, plain_dtype_bytes(dtype)) || !aligned16(topk_idx) || !aligned16(topk_gate)))
+        return KOSMOS_ERR_INVALID_ARG;
+    if (bias != nullptr && !aligned16(bias)) return KOSMOS_ERR_INVALID_ARG;
+    if (expert_counts != nullptr) {
+        if (!aligned16(expert_counts)) return KOSMOS_ERR_INVALID_ARG;
+        if (!aligned16(ws) || ws_bytes < route_workspace_bytes(n_experts)) return KOSMOS_ERR_WORKSPACE;
+    }
+    RouteLaunch L;
+    L.logits = logits; L.dtype = dtype; L.T = tokens; L.ld = ld_logits; L.E = n_experts; L.r = *router;
+    L.bias = bias; L.idx = topk_idx; L.gate = topk_gate; L.counts = expert_counts; L.ws = ws;
+    L.sms = device_sms();
+    if (L.sms < 1) return KOSMOS_ERR_CUDA;
+    return launch_route(L, static_cast<cudaStream_t>(stream));
+}
+
+kosmos_status kosmos_route_bwd(const void *logits, int dtype, int64_t tokens, int n_experts, int64_t ld_logits,
+                               const kosmos_router *router, const int32_t *topk_idx, const float *topk_gate,
+                               const float *dgate, void *dlogits, int64_t ld_dlogits, void *stream) {
+    if (!route_args_ok(dtype, tokens, n_experts, ld_logits, router)) return KOSMOS_ERR_INVALID_ARG;
+    if (ld_dlogits < n_experts || ld_dlogits > (1ll << 32)) return KOSMOS_ERR_INVALID_ARG;
+    if (tokens == 0) return KOSMOS_OK;
+    const int es = plain_dtype_bytes(dtype);
+    if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !aligned16(topk_idx) || !aligned16(topk_gate) ||
+        !aligned16(dgate))
+        return KOSMOS_ERR_INVALID_ARG;
+    RouteBwdLaunch L;
+    L.logits = logits; L.dtype = dtype; L.T = tokens; L.ld = ld_logits; L.ldd = ld_dlogits; L.E = n_experts;
+    L.r = *router; L.idx = topk_idx; L.gate = topk_gate; L.dgate = dgate; L.dlogits = dlogits;
+    L.sms = device_sms();
+    if (L.sms < 1) return KOSMOS_ERR_CUDA;
+    return launch_route_bwd(L, static_cast<cudaStream_t>(stream));
+}
+
+// Sizes and types of a gradient set (n tensors, fewer than 2^46 elements together).
+static bool grad_set_ok(const int64_t *sizes, const int32_t *dtypes, int n) {
+    if (n < 0 || n > 65536 || (n > 0 && (sizes == nullptr || dtypes == nullptr))) return false;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        if (plain_dtype_bytes(dtypes[i]) == 0 || sizes[i] < 0 || sizes[i] >= (1ll << 46)) return false;
+        total += sizes[i];
+        if (total >= (1ll << 46)) return false;
+    }
+    return true;
+}
+
+size_t kosmos_grad_workspace_bytes(const int64_t *sizes, const int32_t *dtypes, int n) {
+    if (!grad_set_ok(sizes, dtypes, n)) return 0;
+    return grad_workspace_bytes(sizes, dtypes, n);
+}
+
+static kosmos_status grad_call(const void *const *grads, void *const *outs, bool clip, const int64_t *sizes,
+                               const int32_t *dtypes, int n, float max_norm, float *norm, float *tensor_norms,
+                               void *ws, size_t ws_bytes, void *stream) {
+    if (!grad_set_ok(sizes, dtypes, n)) return KOSMOS_ERR_INVALID_ARG;
+    if (n > 0 && (grads == nullptr || (clip && outs == nullptr))) return KOSMOS_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        const int es = plain_dtype_bytes(dtypes[i]);
+        if (sizes[i] == 0) continue;
+        if (!aligned_to(grads[i], es) || (clip && !aligned_to(outs[i], es))) return KOSMOS_ERR_INVALID_ARG;
+    }
+    if (!aligned_to(norm, 4) || (tensor_norms != nullptr && !aligned_to(tensor_norms, 4)))
+        return KOSMOS_ERR_INVALID_ARG;
+    if (clip && !(max_norm >= 0.0f && max_norm <= 3.402823466e38f)) return KOSMOS_ERR_INVALID_ARG;
+    if (!aligned16(ws) || ws_bytes < grad_workspace_bytes(sizes, dtypes, n)) return KOSMOS_ERR_WORKSPACE;
+    GradLaunch L;
+    L.grads = grads; L.outs = clip ? outs : nullptr; L.sizes = sizes; L.dtypes = dtypes; L.n = n;
+    L.max_norm = max_norm; L.norm = norm; L.tensor_norms = tensor_norms; L.ws = ws;
+    L.sms = device_sms();
+    if (L.sms < 1) return KOSMOS_ERR_CUDA;
+    return launch_grad(L, static_cast<cudaStream_t>(stream));
+}
+
+kosmos_status kosmos_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes, int n,
+                               float *norm, float *tensor_norms, void *ws, size_t ws_bytes, void *stream) {
+    return grad_call(grads, nullptr, false, sizes, dtypes, n, 0.0f, norm, tensor_norms, ws, ws_bytes, stream);
+}
+
+kosmos_status kosmos_grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
+                               const int32_t *dtypes, int n, float max_norm, float *norm, void *ws, size_t ws_bytes,
+                               void *stream) {
+    return grad_call(grads, outs, true, sizes, dtypes, n, max_norm, norm, nullptr, ws, ws_bytes, stream);
+}
+
 kosmos_status kosmos_status_sync(void *ws, void *stream, int64_t *failing_entry) {
     if (!aligned16(ws)) return KOSMOS_ERR_INVALID_ARG;
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return KOSMOS_ERR_CUDA;

@@ -152,6 +152,51 @@ kosmos_status launch_mxfp8_quantize(const void *x, int64_t rows, int64_t cols, i
 kosmos_status launch_rail_decode(int op, int P, int64_t m, int64_t n, int order, int rank, int rail, int tile_m,
                                  int64_t split,
                                  int32_t *out, int64_t count, cudaStream_t stream);
+// Routing and gradient operators (route.cu, grad.cu): arguments are validated
+// by the C ABI; these pick the kernel variant and launch.
+struct RouteLaunch {
+    const void *logits;
+    int dtype;
+    int64_t T, ld;
+    int E;
+    kosmos_router r;
+    const float *bias;
+    int32_t *idx;
+    float *gate;
+    int32_t *counts;
+    void *ws;
+    int sms;
+};
+kosmos_status launch_route(const RouteLaunch &L, cudaStream_t stream);
+size_t route_workspace_bytes(int E);
+
+struct RouteBwdLaunch {
+    const void *logits;
+    int dtype;
+    int64_t T, ld, ldd;
+    int E;
+    kosmos_router r;
+    const int32_t *idx;
+    const float *gate, *dgate;
+    void *dlogits;
+    int sms;
+};
+kosmos_status launch_route_bwd(const RouteBwdLaunch &L, cudaStream_t stream);
+
+struct GradLaunch {
+    const void *const *grads;
+    void *const *outs;      // nullptr: the norm alone
+    const int64_t *sizes;
+    const int32_t *dtypes;
+    int n;
+    float max_norm;
+    float *norm, *tensor_norms;
+    void *ws;
+    int sms;
+};
+kosmos_status launch_grad(const GradLaunch &L, cudaStream_t stream);
+size_t grad_workspace_bytes(const int64_t *sizes, const int32_t *dtypes, int n);
+
 int ag_pair_grid_limit();
 int ag_mxfp8_pair_grid_limit();
 int rs_pair_grid_limit(bool mx = false);

@@ -62,7 +62,9 @@ typedef enum kosmos_status {
 
 typedef enum kosmos_dtype {
     KOSMOS_BF16 = 0,
-    KOSMOS_MXFP8_E4M3 = 1        /* E4M3 bytes + one E8M0 scale byte per 32 K-elements */
+    KOSMOS_MXFP8_E4M3 = 1,       /* E4M3 bytes + one E8M0 scale byte per 32 K-elements */
+    KOSMOS_FP16 = 2,             /* router and gradient operators only */
+    KOSMOS_FP32 = 3              /* router and gradient operators only */
 } kosmos_dtype;
 
 typedef enum kosmos_op {
@@ -375,6 +377,137 @@ KOSMOS_API kosmos_status kosmos_moe_bwd_debug_view(int what, int P, int64_t toke
  */
 KOSMOS_API kosmos_status kosmos_mxfp8_quantize(const void *x, int64_t rows, int64_t cols, int along_cols,
                                     void *q, void *scales, void *stream);
+
+/* ---------------------------------------------------------------- routing
+ *
+ * The router of an expert layer on its own, for layers whose router is not
+ * the softmax top-K that kosmos_moe_fwd computes inside its launch.  Neither
+ * these operators nor the gradient operators below are on the KOSMOS pages.
+ */
+enum { KOSMOS_SCORE_SOFTMAX = 0, KOSMOS_SCORE_SIGMOID = 1 };
+
+#define KOSMOS_ROUTE_MAX_EXPERTS 1024
+#define KOSMOS_ROUTE_MAX_TOPK 16
+#define KOSMOS_ROUTE_MAX_GROUPS 32
+
+typedef struct kosmos_router {
+    int32_t score;        /* KOSMOS_SCORE_*: p = softmax of the row, or p = 1 / (1 + exp(-logit)) */
+    int32_t topk;         /* experts per token, 1 .. 16, at most topk_groups * n_experts / n_groups */
+    int32_t n_groups;     /* groups of consecutive experts, 1 .. 32, dividing n_experts; 1 = none */
+    int32_t topk_groups;  /* groups that stay open per token, 1 .. n_groups */
+    int32_t group_top;    /* a group's score is the sum of its best group_top selection scores: 1 or 2
+                             (2 needs groups of two experts or more) */
+    int32_t renorm;       /* nonzero: gates are divided by the sum of the chosen p */
+    float scale;          /* factor on the gates, finite and > 0 */
+    int32_t reserved;     /* 0 */
+} kosmos_router;
+
+/* Fills *router with softmax, top-1, no groups (1, 1, 1), renorm, scale 1. */
+KOSMOS_API void kosmos_default_router(kosmos_router *router);
+
+/*
+ * Routing: topk experts and their gates for every token.
+ *
+ *   s[e] = p[e] + bias[e]                       the selection score
+ *   group score = sum of the group's best group_top scores s; the topk_groups
+ *   best groups stay open (ties to the lower group).
+ *   topk_idx = the topk experts of largest s among the open ones, descending,
+ *   ties to the lower expert.  Order and ties are those of s in 64-bit
+ *   arithmetic; without a bias the order of s is the order of the logits.
+ *   gate = scale * p, with renorm scale * p / (sum of the chosen p): the bias
+ *   takes part in the choice only.
+ *
+ *   An expert whose logit (or selection score) is -inf or NaN, or whose group
+ *   is not open, is closed: it is chosen only when fewer than topk experts
+ *   are open, after all of those, in index order, and its gate is 0.  So
+ *   topk_idx always holds topk different experts.  A group's closed experts
+ *   do not count in its score; a group without an open expert ranks last.
+ *   A row with a NaN logit has NaN gates, as has a softmax row with +inf.
+ *
+ *   logits        : [tokens, n_experts], dtype KOSMOS_BF16, KOSMOS_FP16 or
+ *                   KOSMOS_FP32, rows ld_logits >= n_experts elements apart;
+ *                   aligned to its element (rows on 16-byte boundaries are
+ *                   read in 16-byte pieces).
+ *   bias          : [n_experts] fp32, or NULL.
+ *   topk_idx      : out, [tokens, topk] int32.
+ *   topk_gate     : out, [tokens, topk] fp32.
+ *   expert_counts : out, [n_experts] int32: (token, slot) pairs per expert, closed
+ *                   picks included; or NULL.
+ *   ws            : kosmos_route_workspace_bytes(n_experts) bytes, needed with
+ *                   expert_counts only (else NULL, 0); zeroed once by
+ *                   kosmos_workspace_init, ready for the next call after each.
+ *   Requirements: 0 <= tokens <= 2^30, 1 <= n_experts <= 1024, and those of
+ *   kosmos_router.  Scores and sums are fp32 or wider.
+ */
+KOSMOS_API kosmos_status kosmos_route(const void *logits, int dtype, int64_t tokens, int n_experts,
+                                      int64_t ld_logits, const kosmos_router *router, const float *bias,
+                                      int32_t *topk_idx, float *topk_gate, int32_t *expert_counts, void *ws,
+                                      size_t ws_bytes, void *stream);
+
+/* Workspace size in bytes for kosmos_route; 0 for an invalid n_experts. */
+KOSMOS_API size_t kosmos_route_workspace_bytes(int n_experts);
+
+/*
+ * Gradient of kosmos_route's gates, the choice of experts held fixed (the
+ * bias takes part in the choice only, so it has none).  With g the gates, dg
+ * their gradients and D = sum over the chosen of g dg:
+ *   softmax, renorm : dl[j] = g[j] (dg[j] - D / scale)                  j chosen, 0 elsewhere
+ *   softmax         : dl[e] = [e chosen] g[e] dg[e] - p[e] D            every e
+ *   sigmoid, renorm : dl[j] = g[j] (dg[j] - D / scale) (1 - p[j])       j chosen, 0 elsewhere
+ *   sigmoid         : dl[j] = g[j] dg[j] (1 - p[j])                     j chosen, 0 elsewhere
+ *
+ *   logits, dtype, tokens, n_experts, ld_logits, router : as in the forward call
+ *                   (softmax with renorm does not read the logits).
+ *   topk_idx, topk_gate : the forward's outputs; an index outside
+ *                   [0, n_experts) contributes nothing.
+ *   dgate         : [tokens, topk] fp32.
+ *   dlogits       : out, [tokens, n_experts], the logits' type, rows ld_dlogits
+ *                   elements apart; every element is written, rounded once.
+ */
+KOSMOS_API kosmos_status kosmos_route_bwd(const void *logits, int dtype, int64_t tokens, int n_experts,
+                                          int64_t ld_logits, const kosmos_router *router,
+                                          const int32_t *topk_idx, const float *topk_gate, const float *dgate,
+                                          void *dlogits, int64_t ld_dlogits, void *stream);
+
+/* -------------------------------------------------- norm of many gradients
+ *
+ * A gradient set is a list of n tensors: grads[i] with sizes[i] >= 0 elements
+ * of type dtypes[i] (KOSMOS_BF16, KOSMOS_FP16 or KOSMOS_FP32), each aligned to
+ * its element only (a gradient may be a view that starts anywhere in a flat
+ * buffer).  The lists are read during the call and not kept.
+ */
+
+/*
+ * Global norm: norm[0] = sqrt(sum over every tensor of x^2), and
+ * tensor_norms[i] = the norm of tensor i alone (or NULL).  Squares are summed
+ * in fp32 over at most 64 elements and from there in fp64, in an order that
+ * depends on the sizes and the device alone (reruns are bit-identical); sums
+ * that leave fp32's range are taken again in fp64, so that only a norm beyond
+ * fp32 itself is inf.  NaN or inf anywhere gives NaN or inf.
+ *   norm, tensor_norms : out, fp32 device memory.
+ *   ws : kosmos_grad_workspace_bytes of the set; zeroed once by
+ *        kosmos_workspace_init, ready for the next call after each.
+ *   Requirements: 0 <= n <= 65536, the elements of all tensors < 2^46.
+ */
+KOSMOS_API kosmos_status kosmos_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                                          int n, float *norm, float *tensor_norms, void *ws, size_t ws_bytes,
+                                          void *stream);
+
+/*
+ * Clipping: the global norm as above, then
+ *   outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6))
+ * in fp32, rounded once to the tensor's type.  outs[i] may be grads[i] (in
+ * place; nothing is written then when the factor is 1) or memory that overlaps
+ * no tensor of the set.  A NaN norm gives NaN gradients, an infinite one
+ * zeros (NaN where the gradient is infinite).  Finite max_norm >= 0.
+ */
+KOSMOS_API kosmos_status kosmos_grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
+                                          const int32_t *dtypes, int n, float max_norm, float *norm, void *ws,
+                                          size_t ws_bytes, void *stream);
+
+/* Workspace size in bytes for kosmos_grad_norm and kosmos_grad_clip; 0 for
+ * invalid arguments. */
+KOSMOS_API size_t kosmos_grad_workspace_bytes(const int64_t *sizes, const int32_t *dtypes, int n);
 
 /* Size in bytes of the scratch array that kosmos_ag_gemm_noalloc uses. */
 #define KOSMOS_STATIC_WS_BYTES 65536
