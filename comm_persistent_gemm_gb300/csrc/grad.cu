@@ -48,12 +48,51 @@ template <int N> struct GradParams {
     GradTensor t[N];
 };
 
-__device__ __forceinline__ float elem(const float *p) { return *p; }
-__device__ __forceinline__ float elem(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float elem(const __half *p) { return __half2float(*p); }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
+// A tensor's elements in raw 32-bit words, EPW per word.
+template <typename T> struct Words;
+template <> struct Words<float> {
+    static constexpr int EPW = 1;
+    static constexpr uint32_t MAGNITUDE = 0x7FFFFFFFu;  // every bit but the sign
+    static __device__ __forceinline__ void unpack(uint32_t w, float *v) { v[0] = __uint_as_float(w); }
+    static __device__ __forceinline__ uint32_t pack(const float *v) { return __float_as_uint(v[0]); }
+    static __device__ __forceinline__ float load(const float *p) { return *p; }
+    static __device__ __forceinline__ void store(float *p, float v) { *p = v; }
+};
+template <> struct Words<__nv_bfloat16> {
+    static constexpr int EPW = 2;
+    static constexpr uint32_t MAGNITUDE = 0x7FFF7FFFu;
+    static __device__ __forceinline__ void unpack(uint32_t w, float *v) {
+        v[0] = __uint_as_float(w << 16);
+        v[1] = __uint_as_float(w & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ uint32_t pack(const float *v) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[0], v[1]);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    static __device__ __forceinline__ float load(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+};
+template <> struct Words<__half> {
+    static constexpr int EPW = 2;
+    static constexpr uint32_t MAGNITUDE = 0x7FFF7FFFu;
+    static __device__ __forceinline__ void unpack(uint32_t w, float *v) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        v[0] = f.x;
+        v[1] = f.y;
+    }
+    static __device__ __forceinline__ uint32_t pack(const float *v) {
+        const __half2 h = __floats2half2_rn(v[0], v[1]);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float load(const __half *p) { return __half2float(*p); }
+    static __device__ __forceinline__ void store(__half *p, float v) { *p = __float2half_rn(v); }
+};
+
+// Elements before the first 16-byte boundary of x (a tensor may start anywhere).
+template <typename T> __device__ __forceinline__ int64_t head_elems(const T *x, int64_t n) {
+    const int64_t h = ((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / sizeof(T);
+    return h < n ? h : n;
+}
 
 // The last tensor whose first chunk is not after chunk c (empty tensors share
 // their successor's first chunk and are passed over).
@@ -79,18 +118,104 @@ __device__ __forceinline__ double block_sum(double v, double *s_red) {
     return r;
 }
 
-template <typename T> __device__ __forceinline__ double chunk_squares(const T *x, int64_t e0, int64_t e1) {
+// Squares are summed in fp32 over the GRAD_UNROLL vectors that a thread has in
+// flight (at most 64 elements) and in fp64 beyond.  An fp32 sum above HUGE_SUM
+// may have overflowed; one below TINY_SUM that is not of zeros may have lost
+// squares that underflowed (above it, 64 lost halves of 2^-149 are less than
+// 2^-29 of the sum).  Either way the chunk is summed again in fp64.
+constexpr int GRAD_UNROLL = 8;
+constexpr float HUGE_SUM = 1e38f, TINY_SUM = 1e-36f;
+
+__device__ __forceinline__ bool out_of_range(float s, uint32_t any) {
+    return !(s <= HUGE_SUM) || (s < TINY_SUM && any != 0u);
+}
+
+template <typename T> __device__ __forceinline__ double chunk_squares(const T *x, int64_t n) {
+    using Wd = Words<T>;
+    constexpr int VE = 4 * Wd::EPW;  // elements of a vector
+    const int64_t head = head_elems(x, n);
+    const int64_t nv = (n - head) / VE;
+    const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
     double acc = 0.0;
-    for (int64_t i = e0 + threadIdx.x; i < e1; i += GRAD_THREADS) {
-        const double v = elem(x + i);
+    bool redo = false;
+    for (int64_t j0 = threadIdx.x; j0 < nv; j0 += GRAD_UNROLL * GRAD_THREADS) {
+        uint4 w[GRAD_UNROLL];
+#pragma unroll
+        for (int u = 0; u < GRAD_UNROLL; ++u) {
+            const int64_t j = j0 + u * GRAD_THREADS;
+            w[u] = j < nv ? __ldg(xv + j) : make_uint4(0, 0, 0, 0);
+        }
+        float s[2] = {0.f, 0.f};
+        uint32_t any = 0u;
+#pragma unroll
+        for (int u = 0; u < GRAD_UNROLL; ++u) {
+            const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[Wd::EPW];
+                Wd::unpack(ww[i], v);
+#pragma unroll
+                for (int e = 0; e < Wd::EPW; ++e) s[i & 1] = fmaf(v[e], v[e], s[i & 1]);
+                any |= ww[i] & Wd::MAGNITUDE;
+            }
+        }
+        redo = redo || out_of_range(s[0] + s[1], any);
+        acc += static_cast<double>(s[0] + s[1]);
+    }
+    // the elements before and after the vectors: at most 2 * (VE - 1)
+    const int64_t rest = n - nv * VE;
+    if (threadIdx.x < rest) {
+        const int64_t i = threadIdx.x < head ? threadIdx.x : threadIdx.x + nv * VE;
+        const double v = Wd::load(x + i);
         acc += v * v;
+    }
+    if (__syncthreads_or(redo)) {
+        acc = 0.0;
+        for (int64_t i = threadIdx.x; i < n; i += GRAD_THREADS) {
+            const double v = Wd::load(x + i);
+            acc += v * v;
+        }
     }
     return acc;
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T *x, T *out, int64_t e0, int64_t e1, float coef) {
-    for (int64_t i = e0 + threadIdx.x; i < e1; i += GRAD_THREADS) put(out + i, elem(x + i) * coef);
+// One rounding from the fp32 product.  Vectors need x and out at the same
+// place within 16 bytes; otherwise elements are moved one by one.
+template <typename T> __device__ __forceinline__ void chunk_scale(const T *x, T *out, int64_t n, float coef) {
+    using Wd = Words<T>;
+    constexpr int VE = 4 * Wd::EPW;
+    const bool vec = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    const int64_t head = vec ? head_elems(x, n) : 0;
+    const int64_t nv = vec ? (n - head) / VE : 0;
+    const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
+    uint4 *ov = reinterpret_cast<uint4 *>(out + head);
+    for (int64_t j0 = threadIdx.x; j0 < nv; j0 += GRAD_UNROLL * GRAD_THREADS) {
+        uint4 w[GRAD_UNROLL];
+#pragma unroll
+        for (int u = 0; u < GRAD_UNROLL; ++u) {
+            const int64_t j = j0 + u * GRAD_THREADS;
+            if (j < nv) w[u] = xv[j];
+        }
+#pragma unroll
+        for (int u = 0; u < GRAD_UNROLL; ++u) {
+            const int64_t j = j0 + u * GRAD_THREADS;
+            uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[Wd::EPW];
+                Wd::unpack(ww[i], v);
+#pragma unroll
+                for (int e = 0; e < Wd::EPW; ++e) v[e] *= coef;
+                ww[i] = Wd::pack(v);
+            }
+            if (j < nv) ov[j] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
+        }
+    }
+    const int64_t rest = n - nv * VE;
+    for (int64_t r = threadIdx.x; r < rest; r += GRAD_THREADS) {
+        const int64_t i = r < head ? r : r + nv * VE;
+        Wd::store(out + i, Wd::load(x + i) * coef);
+    }
 }
 
 template <int N> __device__ __forceinline__ void chunk_range(const GradParams<N> &p, int i, int c, int64_t &e0,
@@ -110,9 +235,9 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const __grid_co
         int64_t e0, e1;
         chunk_range(p, i, c, e0, e1);
         double v;
-        if (p.t[i].dtype == KOSMOS_BF16) v = chunk_squares(static_cast<const __nv_bfloat16 *>(p.t[i].x), e0, e1);
-        else if (p.t[i].dtype == KOSMOS_FP16) v = chunk_squares(static_cast<const __half *>(p.t[i].x), e0, e1);
-        else v = chunk_squares(static_cast<const float *>(p.t[i].x), e0, e1);
+        if (p.t[i].dtype == KOSMOS_BF16) v = chunk_squares(static_cast<const __nv_bfloat16 *>(p.t[i].x) + e0, e1 - e0);
+        else if (p.t[i].dtype == KOSMOS_FP16) v = chunk_squares(static_cast<const __half *>(p.t[i].x) + e0, e1 - e0);
+        else v = chunk_squares(static_cast<const float *>(p.t[i].x) + e0, e1 - e0);
         v = block_sum(v, s_red);
         if (threadIdx.x == 0) p.part[c] = v;
     }
@@ -156,17 +281,18 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const __grid_co
 template <int N>
 __global__ void __launch_bounds__(GRAD_THREADS) grad_scale_kernel(const __grid_constant__ GradParams<N> p) {
     const float coef = p.scr->coef;
-    for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+    // from the back, where the norm's pass ended: what it read last is still in L2
+    for (int c = p.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
         const int i = tensor_of(p, c);
         if (coef == 1.0f && p.t[i].out == p.t[i].x) continue;
         int64_t e0, e1;
         chunk_range(p, i, c, e0, e1);
         if (p.t[i].dtype == KOSMOS_BF16)
-            chunk_scale(static_cast<const __nv_bfloat16 *>(p.t[i].x), static_cast<__nv_bfloat16 *>(p.t[i].out), e0, e1, coef);
+            chunk_scale(static_cast<const __nv_bfloat16 *>(p.t[i].x) + e0, static_cast<__nv_bfloat16 *>(p.t[i].out) + e0, e1 - e0, coef);
         else if (p.t[i].dtype == KOSMOS_FP16)
-            chunk_scale(static_cast<const __half *>(p.t[i].x), static_cast<__half *>(p.t[i].out), e0, e1, coef);
+            chunk_scale(static_cast<const __half *>(p.t[i].x) + e0, static_cast<__half *>(p.t[i].out) + e0, e1 - e0, coef);
         else
-            chunk_scale(static_cast<const float *>(p.t[i].x), static_cast<float *>(p.t[i].out), e0, e1, coef);
+            chunk_scale(static_cast<const float *>(p.t[i].x) + e0, static_cast<float *>(p.t[i].out) + e0, e1 - e0, coef);
     }
 }
 
