@@ -167,7 +167,9 @@ def opts(**kw) -> Opts:
 def _stream(stream) -> Optional[int]:
     import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current device's current stream without building a Stream
+        # object for it (0.3 instead of 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -384,33 +386,39 @@ def router(topk: int, score: int = SCORE_SOFTMAX, n_groups: int = 1, topk_groups
     return r
 
 
+_plain_dtypes = {}
+
+
 def _plain_dtype(t) -> int:
-    import torch
-    d = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(t.dtype)
+    if not _plain_dtypes:
+        import torch
+        _plain_dtypes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+    d = _plain_dtypes.get(t.dtype)
     if d is None:
         raise ValueError(f"kosmos: bf16, fp16 or fp32 expected, not {t.dtype}")
     return d
 
 
 def _check_like(what: str, t, dtype, shape):
-    """t (or None): a contiguous CUDA tensor of this type and shape."""
-    if t is None:
-        return
-    if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} and shape {tuple(shape)} expected, got "
+    """t: a contiguous CUDA tensor of this type and shape."""
+    if not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} and shape {shape} expected, got "
                          f"{t.dtype} {tuple(t.shape)}")
 
 
-def _check_rows(what: str, t):
-    """t: a CUDA matrix whose rows are contiguous (any row stride)."""
-    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a CUDA matrix with contiguous rows expected")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{what}: rows overlap (row stride {t.stride(0)} < {t.shape[1]} columns)")
-
-
-def _ld(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(what: str, t):
+    """(rows, columns, row stride) of a CUDA matrix whose rows are contiguous
+    and do not overlap."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{what}: a CUDA matrix expected")
+    (n, m), (ld, st) = t.shape, t.stride()
+    if m > 1 and st != 1:
+        raise ValueError(f"{what}: rows are not contiguous")
+    if n <= 1:
+        return n, m, m
+    if ld < m:
+        raise ValueError(f"{what}: rows overlap (row stride {ld}, {m} columns)")
+    return n, m, ld
 
 
 def route_workspace(n_experts: int, device=None):
@@ -429,18 +437,23 @@ def route(logits, r: Router, topk_idx, topk_gate, bias=None, expert_counts=None,
     expert_counts [experts] int32 receives the tokens per expert and needs
     ws = route_workspace(experts)."""
     import torch
-    _check_rows("route: logits", logits)
-    T, E = logits.shape
-    _check_like("route: topk_idx", topk_idx, torch.int32, (T, r.topk))
-    _check_like("route: topk_gate", topk_gate, torch.float32, (T, r.topk))
-    _check_like("route: bias", bias, torch.float32, (E,))
-    _check_like("route: expert_counts", expert_counts, torch.int32, (E,))
-    _check_cuda(ws)
-    rc = lib().kosmos_route(logits.data_ptr(), _plain_dtype(logits), T, E, _ld(logits), C.byref(r),
-                            bias.data_ptr() if bias is not None else None, topk_idx.data_ptr(), topk_gate.data_ptr(),
-                            expert_counts.data_ptr() if expert_counts is not None else None,
-                            ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
-                            _stream(stream))
+    T, E, ld = _rows("route: logits", logits)
+    shape = (T, r.topk)
+    _check_like("route: topk_idx", topk_idx, torch.int32, shape)
+    _check_like("route: topk_gate", topk_gate, torch.float32, shape)
+    b = c = w = None
+    nbytes = 0
+    if bias is not None:
+        _check_like("route: bias", bias, torch.float32, (E,))
+        b = bias.data_ptr()
+    if expert_counts is not None:
+        _check_like("route: expert_counts", expert_counts, torch.int32, (E,))
+        c = expert_counts.data_ptr()
+    if ws is not None:
+        _check_cuda(ws)
+        w, nbytes = ws.data_ptr(), ws.numel()
+    rc = lib().kosmos_route(logits.data_ptr(), _plain_dtype(logits), T, E, ld, r, b, topk_idx.data_ptr(),
+                            topk_gate.data_ptr(), c, w, nbytes, _stream(stream))
     _raise(rc, "kosmos_route")
 
 
@@ -448,17 +461,16 @@ def route_bwd(logits, r: Router, topk_idx, topk_gate, dgate, dlogits, stream=Non
     """dlogits (the logits' type) from dgate: the gradient of route's gates
     with the choice of experts held fixed."""
     import torch
-    _check_rows("route_bwd: logits", logits)
-    _check_rows("route_bwd: dlogits", dlogits)
-    T, E = logits.shape
-    if dlogits.dtype != logits.dtype or tuple(dlogits.shape) != (T, E):
+    T, E, ld = _rows("route_bwd: logits", logits)
+    T2, E2, ldd = _rows("route_bwd: dlogits", dlogits)
+    if dlogits.dtype is not logits.dtype or T2 != T or E2 != E:
         raise ValueError("route_bwd: dlogits needs the logits' type and shape")
-    _check_like("route_bwd: topk_idx", topk_idx, torch.int32, (T, r.topk))
-    _check_like("route_bwd: topk_gate", topk_gate, torch.float32, (T, r.topk))
-    _check_like("route_bwd: dgate", dgate, torch.float32, (T, r.topk))
-    rc = lib().kosmos_route_bwd(logits.data_ptr(), _plain_dtype(logits), T, E, _ld(logits), C.byref(r),
-                                topk_idx.data_ptr(), topk_gate.data_ptr(), dgate.data_ptr(), dlogits.data_ptr(),
-                                _ld(dlogits), _stream(stream))
+    shape = (T, r.topk)
+    _check_like("route_bwd: topk_idx", topk_idx, torch.int32, shape)
+    _check_like("route_bwd: topk_gate", topk_gate, torch.float32, shape)
+    _check_like("route_bwd: dgate", dgate, torch.float32, shape)
+    rc = lib().kosmos_route_bwd(logits.data_ptr(), _plain_dtype(logits), T, E, ld, r, topk_idx.data_ptr(),
+                                topk_gate.data_ptr(), dgate.data_ptr(), dlogits.data_ptr(), ldd, _stream(stream))
     _raise(rc, "kosmos_route_bwd")
 
 
@@ -505,11 +517,13 @@ def grad_norm(grads, norm, ws, tensor_norms=None, stream=None):
     import torch
     s = _grad_set(grads)
     _check_like("grad_norm: norm", norm, torch.float32, (1,))
-    _check_like("grad_norm: tensor_norms", tensor_norms, torch.float32, (s.n,))
+    each = None
+    if tensor_norms is not None:
+        _check_like("grad_norm: tensor_norms", tensor_norms, torch.float32, (s.n,))
+        each = tensor_norms.data_ptr()
     _check_cuda(ws)
-    rc = lib().kosmos_grad_norm(s.ptrs, s.sizes, s.dtypes, s.n, norm.data_ptr(),
-                                tensor_norms.data_ptr() if tensor_norms is not None else None, ws.data_ptr(),
-                                ws.numel(), _stream(stream))
+    rc = lib().kosmos_grad_norm(s.ptrs, s.sizes, s.dtypes, s.n, norm.data_ptr(), each, ws.data_ptr(), ws.numel(),
+                                _stream(stream))
     _raise(rc, "kosmos_grad_norm")
 
 

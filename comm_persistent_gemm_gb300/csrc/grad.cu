@@ -17,7 +17,7 @@ namespace kosmos {
 namespace {
 
 constexpr int GRAD_THREADS = 256;
-constexpr int GRAD_MAX_T = 1000;             // descriptors of one launch: 32,000 bytes of kernel parameter
+constexpr int GRAD_MAX_T = 1000;             // tensors of one launch: 29 KB of the 32,764 bytes of kernel parameter
 constexpr int64_t GRAD_MIN_CHUNK = 16384;    // bytes: one pass of a block's 16-byte loads, four per thread
 constexpr int64_t GRAD_CHUNKS = 9728;        // chunks of a large set
 
@@ -25,8 +25,6 @@ struct GradTensor {
     const void *x;
     void *out;
     int64_t n;        // elements
-    int32_t chunk0;   // this tensor's first chunk within the launch
-    int32_t dtype;
 };
 
 // Workspace: the 256-byte header (its done_ctas counts finished blocks), then
@@ -45,6 +43,8 @@ template <int N> struct GradParams {
     int nt, chunks;
     int first, last;              // the launch begins / ends the set
     float max_norm;
+    int32_t chunk0[N + 1];        // each tensor's first chunk within the launch, then the chunks' number
+    uint8_t dtype[N];
     GradTensor t[N];
 };
 
@@ -100,7 +100,7 @@ template <int N> __device__ __forceinline__ int tensor_of(const GradParams<N> &p
     int lo = 0, hi = p.nt - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.t[mid].chunk0 <= c) lo = mid; else hi = mid - 1;
+        if (p.chunk0[mid] <= c) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
@@ -109,13 +109,15 @@ template <int N> __device__ __forceinline__ int tensor_of(const GradParams<N> &p
 __device__ __forceinline__ double block_sum(double v, double *s_red) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    __syncthreads();  // s_red is free again
     if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
     __syncthreads();
-    double r = 0.0;
-    if (threadIdx.x == 0)
-        for (int i = 0; i < GRAD_THREADS / 32; ++i) r += s_red[i];
-    __syncthreads();
-    return r;
+    if (threadIdx.x < 32) {
+        v = threadIdx.x < GRAD_THREADS / 32 ? s_red[threadIdx.x] : 0.0;
+#pragma unroll
+        for (int d = GRAD_THREADS / 64; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    }
+    return v;
 }
 
 // Squares are summed in fp32 over the GRAD_UNROLL vectors that a thread has in
@@ -130,20 +132,35 @@ __device__ __forceinline__ bool out_of_range(float s, uint32_t any) {
     return !(s <= HUGE_SUM) || (s < TINY_SUM && any != 0u);
 }
 
+// Volatile, so that the loads of a batch are issued together ahead of its
+// arithmetic.
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 template <typename T> __device__ __forceinline__ double chunk_squares(const T *x, int64_t n) {
     using Wd = Words<T>;
     constexpr int VE = 4 * Wd::EPW;  // elements of a vector
     const int64_t head = head_elems(x, n);
-    const int64_t nv = (n - head) / VE;
+    const int nv = static_cast<int>((n - head) / VE);  // a chunk has fewer than 2^31 vectors: 2^46 elements / 9728 / 4
     const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
     double acc = 0.0;
     bool redo = false;
-    for (int64_t j0 = threadIdx.x; j0 < nv; j0 += GRAD_UNROLL * GRAD_THREADS) {
+    for (int j0 = threadIdx.x; j0 < nv; j0 += GRAD_UNROLL * GRAD_THREADS) {
         uint4 w[GRAD_UNROLL];
+        if (j0 + (GRAD_UNROLL - 1) * GRAD_THREADS < nv) {
 #pragma unroll
-        for (int u = 0; u < GRAD_UNROLL; ++u) {
-            const int64_t j = j0 + u * GRAD_THREADS;
-            w[u] = j < nv ? __ldg(xv + j) : make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < GRAD_UNROLL; ++u) w[u] = ld_stream(xv + j0 + u * GRAD_THREADS);
+        } else {
+#pragma unroll
+            for (int u = 0; u < GRAD_UNROLL; ++u) {
+                const int j = j0 + u * GRAD_THREADS;
+                w[u] = make_uint4(0, 0, 0, 0);
+                if (j < nv) w[u] = ld_stream(xv + j);
+            }
         }
         float s[2] = {0.f, 0.f};
         uint32_t any = 0u;
@@ -163,9 +180,9 @@ template <typename T> __device__ __forceinline__ double chunk_squares(const T *x
         acc += static_cast<double>(s[0] + s[1]);
     }
     // the elements before and after the vectors: at most 2 * (VE - 1)
-    const int64_t rest = n - nv * VE;
+    const int64_t rest = n - static_cast<int64_t>(nv) * VE;
     if (threadIdx.x < rest) {
-        const int64_t i = threadIdx.x < head ? threadIdx.x : threadIdx.x + nv * VE;
+        const int64_t i = threadIdx.x < head ? threadIdx.x : threadIdx.x + static_cast<int64_t>(nv) * VE;
         const double v = Wd::load(x + i);
         acc += v * v;
     }
@@ -179,6 +196,16 @@ template <typename T> __device__ __forceinline__ double chunk_squares(const T *x
     return acc;
 }
 
+constexpr int SCALE_UNROLL = 4;
+
+// A value's last use: it should not push others out of the caches.
+__device__ __forceinline__ uint4 ld_last(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 // One rounding from the fp32 product.  Vectors need x and out at the same
 // place within 16 bytes; otherwise elements are moved one by one.
 template <typename T> __device__ __forceinline__ void chunk_scale(const T *x, T *out, int64_t n, float coef) {
@@ -186,42 +213,60 @@ template <typename T> __device__ __forceinline__ void chunk_scale(const T *x, T 
     constexpr int VE = 4 * Wd::EPW;
     const bool vec = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
     const int64_t head = vec ? head_elems(x, n) : 0;
-    const int64_t nv = vec ? (n - head) / VE : 0;
+    const int nv = vec ? static_cast<int>((n - head) / VE) : 0;
     const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
     uint4 *ov = reinterpret_cast<uint4 *>(out + head);
-    for (int64_t j0 = threadIdx.x; j0 < nv; j0 += GRAD_UNROLL * GRAD_THREADS) {
-        uint4 w[GRAD_UNROLL];
+    auto scaled = [coef](uint4 w) {
+        uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int u = 0; u < GRAD_UNROLL; ++u) {
-            const int64_t j = j0 + u * GRAD_THREADS;
-            if (j < nv) w[u] = xv[j];
+        for (int i = 0; i < 4; ++i) {
+            float v[Wd::EPW];
+            Wd::unpack(ww[i], v);
+#pragma unroll
+            for (int e = 0; e < Wd::EPW; ++e) v[e] *= coef;
+            ww[i] = Wd::pack(v);
         }
+        return make_uint4(ww[0], ww[1], ww[2], ww[3]);
+    };
+    int j = threadIdx.x;
+    for (; j + (SCALE_UNROLL - 1) * GRAD_THREADS < nv; j += SCALE_UNROLL * GRAD_THREADS) {
+        uint4 w[SCALE_UNROLL];
 #pragma unroll
-        for (int u = 0; u < GRAD_UNROLL; ++u) {
-            const int64_t j = j0 + u * GRAD_THREADS;
-            uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        for (int u = 0; u < SCALE_UNROLL; ++u) w[u] = ld_last(xv + j + u * GRAD_THREADS);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v[Wd::EPW];
-                Wd::unpack(ww[i], v);
-#pragma unroll
-                for (int e = 0; e < Wd::EPW; ++e) v[e] *= coef;
-                ww[i] = Wd::pack(v);
-            }
-            if (j < nv) ov[j] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
-        }
+        for (int u = 0; u < SCALE_UNROLL; ++u) __stcs(ov + j + u * GRAD_THREADS, scaled(w[u]));
     }
-    const int64_t rest = n - nv * VE;
+    for (; j < nv; j += GRAD_THREADS) __stcs(ov + j, scaled(ld_last(xv + j)));
+    const int64_t rest = n - static_cast<int64_t>(nv) * VE;
     for (int64_t r = threadIdx.x; r < rest; r += GRAD_THREADS) {
-        const int64_t i = r < head ? r : r + nv * VE;
+        const int64_t i = r < head ? r : r + static_cast<int64_t>(nv) * VE;
         Wd::store(out + i, Wd::load(x + i) * coef);
     }
 }
 
-template <int N> __device__ __forceinline__ void chunk_range(const GradParams<N> &p, int i, int c, int64_t &e0,
-                                                             int64_t &e1) {
-    const int64_t per = p.chunk_bytes / (p.t[i].dtype == KOSMOS_FP32 ? 4 : 2);
-    e0 = (c - p.t[i].chunk0) * per;
+// sqrt of an fp64 sum to fp32: the root is taken in fp32 where the sum is in
+// its range (two roundings, 1.5 steps in all; the chain of an fp64 root costs
+// the last block, which everything waits for, longer than its memory accesses).
+__device__ __forceinline__ float sqrt_f32(double v) {
+    if (v > 1e-30 && v < 1e37) return sqrtf(static_cast<float>(v));
+    return static_cast<float>(sqrt(v));
+}
+
+// min(1, max_norm / (norm + 1e-6)) in fp32, or in fp64 where the norm is
+// beyond fp32; a NaN norm gives NaN.
+__device__ __forceinline__ float clip_factor(float max_norm, float norm, double v) {
+    if (norm < 1e30f) {
+        const float f = max_norm / (norm + 1e-6f);
+        return f > 1.0f ? 1.0f : f;
+    }
+    const double f = static_cast<double>(max_norm) / (sqrt(v) + 1e-6);
+    return f > 1.0 ? 1.0f : static_cast<float>(f);
+}
+
+template <int N>
+__device__ __forceinline__ void chunk_range(const GradParams<N> &p, int i, int c, int64_t &e0, int64_t &e1) {
+    const int64_t per = p.chunk_bytes / (p.dtype[i] == KOSMOS_FP32 ? 4 : 2);
+    e0 = (c - p.chunk0[i]) * per;
     e1 = e0 + per < p.t[i].n ? e0 + per : p.t[i].n;
 }
 
@@ -230,49 +275,61 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const __grid_co
     __shared__ double s_red[GRAD_THREADS / 32];
     __shared__ double s_sum[N];
     __shared__ int s_last;
+    // Blocks take every gridDim-th chunk, so that the whole grid reads one
+    // stretch of memory at a time.
     for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
         const int i = tensor_of(p, c);
         int64_t e0, e1;
         chunk_range(p, i, c, e0, e1);
         double v;
-        if (p.t[i].dtype == KOSMOS_BF16) v = chunk_squares(static_cast<const __nv_bfloat16 *>(p.t[i].x) + e0, e1 - e0);
-        else if (p.t[i].dtype == KOSMOS_FP16) v = chunk_squares(static_cast<const __half *>(p.t[i].x) + e0, e1 - e0);
+        if (p.dtype[i] == KOSMOS_BF16) v = chunk_squares(static_cast<const __nv_bfloat16 *>(p.t[i].x) + e0, e1 - e0);
+        else if (p.dtype[i] == KOSMOS_FP16) v = chunk_squares(static_cast<const __half *>(p.t[i].x) + e0, e1 - e0);
         else v = chunk_squares(static_cast<const float *>(p.t[i].x) + e0, e1 - e0);
         v = block_sum(v, s_red);
         if (threadIdx.x == 0) p.part[c] = v;
     }
-    // the last block joins the chunks, tensor by tensor, in their order
     if (threadIdx.x == 0) {
         __threadfence();
         s_last = atomicAdd(&p.hdr->done_ctas, 1u) == gridDim.x - 1;
     }
     __syncthreads();
     if (!s_last) return;
+    // The last block joins the chunks, tensor by tensor, in their order: a
+    // thread takes a tensor of few chunks (a set of many small tensors then
+    // waits for memory once, not once per tensor), a warp one of many.
+    constexpr int FEW = 8;
     __threadfence();
-    const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < p.nt; i += GRAD_THREADS / 32) {
-        const int c1 = i + 1 < p.nt ? p.t[i + 1].chunk0 : p.chunks;
+    for (int j = threadIdx.x; j < p.nt; j += GRAD_THREADS) {
+        const int b = p.chunk0[j], e = p.chunk0[j + 1];
+        if (e - b > FEW) continue;
         double v = 0.0;
-        for (int c = p.t[i].chunk0 + lane; c < c1; c += 32) v += __ldcg(&p.part[c]);
+        for (int c = b; c < e; ++c) v += __ldcg(&p.part[c]);
+        s_sum[j] = v;
+    }
+    const int lane = threadIdx.x & 31;
+    for (int j = threadIdx.x >> 5; j < p.nt; j += GRAD_THREADS / 32) {
+        const int b = p.chunk0[j], e = p.chunk0[j + 1];
+        if (e - b <= FEW) continue;
+        double v = 0.0;
+        for (int c = b + lane; c < e; c += 32) v += __ldcg(&p.part[c]);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-        if (lane == 0) {
-            s_sum[i] = v;
-            if (p.tensor_norms != nullptr) p.tensor_norms[i] = static_cast<float>(sqrt(v));
-        }
+        if (lane == 0) s_sum[j] = v;
     }
     __syncthreads();
     double v = 0.0;
-    for (int i = threadIdx.x; i < p.nt; i += GRAD_THREADS) v += s_sum[i];
+    for (int j = threadIdx.x; j < p.nt; j += GRAD_THREADS) {
+        v += s_sum[j];
+        if (p.tensor_norms != nullptr) p.tensor_norms[j] = sqrt_f32(s_sum[j]);
+    }
     v = block_sum(v, s_red);
     if (threadIdx.x == 0) {
         if (!p.first) v += p.scr->total;
         p.scr->total = v;
         if (p.last) {
-            const double norm = sqrt(v);
-            p.norm[0] = static_cast<float>(norm);
-            const double f = static_cast<double>(p.max_norm) / (norm + 1e-6);
-            p.scr->coef = f > 1.0 ? 1.0f : static_cast<float>(f);  // a NaN stays a NaN
+            const float norm = sqrt_f32(v);
+            p.norm[0] = norm;
+            p.scr->coef = clip_factor(p.max_norm, norm, v);
         }
         p.hdr->done_ctas = 0u;
     }
@@ -282,14 +339,15 @@ template <int N>
 __global__ void __launch_bounds__(GRAD_THREADS) grad_scale_kernel(const __grid_constant__ GradParams<N> p) {
     const float coef = p.scr->coef;
     // from the back, where the norm's pass ended: what it read last is still in L2
-    for (int c = p.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+    for (int c = p.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
         const int i = tensor_of(p, c);
         if (coef == 1.0f && p.t[i].out == p.t[i].x) continue;
         int64_t e0, e1;
         chunk_range(p, i, c, e0, e1);
-        if (p.t[i].dtype == KOSMOS_BF16)
-            chunk_scale(static_cast<const __nv_bfloat16 *>(p.t[i].x) + e0, static_cast<__nv_bfloat16 *>(p.t[i].out) + e0, e1 - e0, coef);
-        else if (p.t[i].dtype == KOSMOS_FP16)
+        if (p.dtype[i] == KOSMOS_BF16)
+            chunk_scale(static_cast<const __nv_bfloat16 *>(p.t[i].x) + e0, static_cast<__nv_bfloat16 *>(p.t[i].out) + e0,
+                        e1 - e0, coef);
+        else if (p.dtype[i] == KOSMOS_FP16)
             chunk_scale(static_cast<const __half *>(p.t[i].x) + e0, static_cast<__half *>(p.t[i].out) + e0, e1 - e0, coef);
         else
             chunk_scale(static_cast<const float *>(p.t[i].x) + e0, static_cast<float *>(p.t[i].out) + e0, e1 - e0, coef);
@@ -327,15 +385,18 @@ template <int N> kosmos_status launch_grad_n(const GradLaunch &L, int64_t chunk_
                 t.x = L.grads[i0 + i];
                 t.out = L.outs != nullptr ? L.outs[i0 + i] : nullptr;
                 t.n = L.sizes[i0 + i];
-                t.dtype = L.dtypes[i0 + i];
-                t.chunk0 = static_cast<int32_t>(chunks);
-                chunks += cdiv(t.n * elem_bytes(t.dtype), chunk_bytes);
+                p.dtype[i] = static_cast<uint8_t>(L.dtypes[i0 + i]);
+                p.chunk0[i] = static_cast<int32_t>(chunks);
+                chunks += cdiv(t.n * elem_bytes(p.dtype[i]), chunk_bytes);
             }
+            p.chunk0[nt] = static_cast<int32_t>(chunks);
             p.nt = nt;
             p.chunks = static_cast<int>(chunks);
             p.first = i0 == 0;
             p.last = i0 + nt >= L.n;
             p.tensor_norms = L.tensor_norms != nullptr ? L.tensor_norms + i0 : nullptr;
+            // four blocks per SM: 1.2 GB clipped in 553 us, against 585 us with two
+            // and 559 us with eight (norm of 4.8 GB: 660 us, 709 us with two)
             int64_t blocks = chunks < 4ll * L.sms ? chunks : 4ll * L.sms;
             if (blocks < 1) blocks = 1;
             if (pass == 0)
