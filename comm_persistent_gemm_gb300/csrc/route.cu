@@ -21,6 +21,13 @@ namespace {
 constexpr int ROUTE_WARPS = 8;
 constexpr int ROUTE_THREADS = ROUTE_WARPS * 32;
 constexpr uint32_t FULL = 0xFFFFFFFFu;
+#ifndef MINB
+#define MINB 3
+#endif
+#ifndef RRF
+#define RRF 32
+#endif
+constexpr int ROUTE_ROWS_FROM = RRF;  // tokens per SM from which a warp takes several rows at a time
 
 struct RouteParams {
     const void *logits;
@@ -36,6 +43,8 @@ struct RouteParams {
     // set by the launcher
     bool vec;                         // runs of experts are loaded whole
     int hist_words, row_words;        // shared memory: counts, then a row of values per warp (groups only)
+    int rows, slots;                  // rows a warp takes at a time, lanes that hold a row's choices
+    bool lane_groups;                 // a group is a run of 1 << lp_log2 lanes
     int gs, gsp, gmul, lp_log2;       // group size, its stride in shared memory, division by gs, lanes per group
 };
 
@@ -47,14 +56,13 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// The expert of lane l's value v: runs of W consecutive experts per lane.
-template <int V, int W> __device__ __forceinline__ int expert_of(int lane, int v) {
-    return (v / W) * 32 * W + lane * W + v % W;
-}
+// Lane l holds the V consecutive experts from l * V on: the lowest of tied
+// experts is then in the lowest lane, and a group is often a run of lanes.
+template <int V> __device__ __forceinline__ int expert_of(int lane, int v) { return lane * V + v; }
 
-__device__ __forceinline__ double warp_max(double v) {
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmax(v, __shfl_xor_sync(FULL, v, d));
+    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, d));
     return v;
 }
 template <typename F> __device__ __forceinline__ F warp_sum(F v) {
@@ -62,110 +70,7 @@ template <typename F> __device__ __forceinline__ F warp_sum(F v) {
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(FULL, v, d);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, d));
-    return v;
-}
-
-// (value, index) pairs ordered by descending value, then ascending index.
-__device__ __forceinline__ bool before(double a, int ia, double b, int ib) { return a > b || (a == b && ia < ib); }
-
-// Chooses the row's experts by their 64-bit selection scores; lane j < k gets
-// the j-th expert and whether it is open.
-template <typename T, int V, int W>
-__device__ __noinline__ void choose_f64(const RouteParams &p, const T *row, int lane, int &my_e, bool &my_open) {
-    double s[V];
-    double m = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = expert_of<V, W>(lane, v);
-        const float x = e < p.E ? to_f32(row[e]) : -INFINITY;
-        s[v] = x;
-        m = fmax(m, s[v]);  // fmax skips NaN
-    }
-    // without a bias s rises with the logit, which then orders the experts
-    // exactly; a sum of two scores needs the scores themselves
-    const bool by_logit = p.bias == nullptr;
-    const bool scores = !by_logit || (p.GK < p.G && p.group_top == 2);
-    if (!scores) {
-    } else if (p.score == KOSMOS_SCORE_SOFTMAX) {
-        m = warp_max(m);
-        double z = 0.0;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (!isnan(s[v])) z += exp(s[v] - m);
-        z = warp_sum(z);
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = s[v] == -INFINITY ? -INFINITY : exp(s[v] - m) / z;
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = s[v] == -INFINITY ? -INFINITY : 1.0 / (1.0 + exp(-s[v]));
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = expert_of<V, W>(lane, v);
-        if (p.bias != nullptr && e < p.E) s[v] += static_cast<double>(p.bias[e]);
-        if (isnan(s[v])) s[v] = -INFINITY;
-    }
-    if (p.GK < p.G) {
-        const int gs = p.E / p.G;
-        double score = -INFINITY;  // lane g: the score of group g
-        for (int g = 0; g < p.G; ++g) {
-            double t1 = -INFINITY, t2 = -INFINITY;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = expert_of<V, W>(lane, v);
-                if (e >= g * gs && e < (g + 1) * gs) {
-                    if (s[v] > t1) { t2 = t1; t1 = s[v]; }
-                    else if (s[v] > t2) t2 = s[v];
-                }
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
-                const double o1 = __shfl_xor_sync(FULL, t1, d), o2 = __shfl_xor_sync(FULL, t2, d);
-                t2 = fmax(fmin(t1, o1), fmax(t2, o2));
-                t1 = fmax(t1, o1);
-            }
-            if (p.group_top == 2 && t2 != -INFINITY) t1 += t2;
-            if (lane == g) score = t1;
-        }
-        int rank = 0;
-        for (int g = 0; g < p.G; ++g) {
-            const double o = __shfl_sync(FULL, score, g);
-            if (before(o, g, score, lane)) ++rank;
-        }
-        const uint32_t open = __ballot_sync(FULL, lane < p.G && rank < p.GK);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = expert_of<V, W>(lane, v);
-            if (e < p.E && !((open >> (e / gs)) & 1u)) s[v] = -INFINITY;
-            else if (e < p.E && by_logit && s[v] != -INFINITY) s[v] = to_f32(row[e]);
-        }
-    }
-    double last = INFINITY;
-    int last_e = -1;
-    for (int j = 0; j < p.k; ++j) {
-        double b = -INFINITY;
-        int be = 0x7FFFFFFF;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = expert_of<V, W>(lane, v);
-            if (e < p.E && before(last, last_e, s[v], e) && before(s[v], e, b, be)) { b = s[v]; be = e; }
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            const double o = __shfl_xor_sync(FULL, b, d);
-            const int oe = __shfl_xor_sync(FULL, be, d);
-            if (before(o, oe, b, be)) { b = o; be = oe; }
-        }
-        if (lane == j) { my_e = be; my_open = b != -INFINITY; }
-        last = b;
-        last_e = be;
-    }
-}
-
-// The gates of the chosen experts (lane j < k: expert of logit x, open or
+// The gates of the chosen experts (p.slots lanes per row; logit x, open or
 // closed).  m, z: the row's maximum and sum of exponentials (softmax without
 // renorm).  Ratios of p are taken relative to the largest chosen one, so that
 // small scores keep their precision.
@@ -175,8 +80,7 @@ __device__ __forceinline__ float route_gate(const RouteParams &p, float x, bool 
         return p.scale * (p.score == KOSMOS_SCORE_SOFTMAX ? expf(x - m) / z : 1.0f / (1.0f + expf(-x)));
     }
     float top = open ? x : -INFINITY;
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
+    for (int d = p.slots / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
     float w = 0.f;
     if (open) {
         if (p.score == KOSMOS_SCORE_SOFTMAX) {
@@ -187,8 +91,7 @@ __device__ __forceinline__ float route_gate(const RouteParams &p, float x, bool 
         }
     }
     float sum = w;
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
+    for (int d = p.slots / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
     return open ? p.scale * (w / sum) : 0.f;
 }
 
@@ -203,8 +106,9 @@ __device__ __forceinline__ float route_gate(const RouteParams &p, float x, bool 
 //               than the scores' rounding error are chosen again in 64 bits.
 enum RouteMode : int { BY_LOGIT16 = 0, BY_LOGIT32 = 1, BY_SCORE = 2 };
 
-// Order-preserving map of floats to unsigned integers (-0 as +0); every real
-// expert's key is above KEY_NONE, closed ones have the key of -inf.
+// Order-preserving map of floats to unsigned integers (-0 as +0).  Closed
+// experts have the key of -inf, and so have the places beyond E, which
+// come last of all because ties go to the lower expert.
 constexpr uint32_t KEY_NONE = 0u, KEY_CLOSED = 0x007FFFFFu, LOW13 = 0x1FFFu;
 __device__ __forceinline__ uint32_t float_key(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);
@@ -214,25 +118,29 @@ __device__ __forceinline__ float key_float(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-// Row t's values: runs of W consecutive experts per lane, in one load each
-// where rows start on multiples of the run.  Beyond E: -inf.
-template <typename T, int V, int W>
-__device__ __forceinline__ void load_row(const T *row, int E, int lane, bool vec, float *x) {
+// A row's values, in loads of up to 16 bytes where rows and runs allow it.
+// Beyond E: -inf.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T *row, int E, int lane, bool vec, T *r) {
+    constexpr int W = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
 #pragma unroll
-    for (int c = 0; c < V / W; ++c) {
-        const int e0 = c * 32 * W + lane * W;
-        alignas(16) T r[W];
+    for (int c = 0; c < V; c += W) {
+        const int e0 = lane * V + c;
         if (vec) {
             if (e0 < E) {
-                if constexpr (sizeof(r) == 16) *reinterpret_cast<uint4 *>(r) = *reinterpret_cast<const uint4 *>(row + e0);
-                else if constexpr (sizeof(r) == 8) *reinterpret_cast<uint2 *>(r) = *reinterpret_cast<const uint2 *>(row + e0);
-                else *reinterpret_cast<uint32_t *>(r) = *reinterpret_cast<const uint32_t *>(row + e0);
-            }
+                if constexpr (W * sizeof(T) == 16)
+                    *reinterpret_cast<uint4 *>(r + c) = __ldg(reinterpret_cast<const uint4 *>(row + e0));
+                else if constexpr (W * sizeof(T) == 8)
+                    *reinterpret_cast<uint2 *>(r + c) = __ldg(reinterpret_cast<const uint2 *>(row + e0));
+                else
+                    *reinterpret_cast<uint32_t *>(r + c) = __ldg(reinterpret_cast<const uint32_t *>(row + e0));
+            } else {
 #pragma unroll
-            for (int i = 0; i < W; ++i) x[c * W + i] = e0 < E ? to_f32(r[i]) : -INFINITY;
+                for (int i = 0; i < W; ++i) r[c + i] = from_f32<T>(-INFINITY);
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < W; ++i) x[c * W + i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
+            for (int i = 0; i < W; ++i) r[c + i] = e0 + i < E ? row[e0 + i] : from_f32<T>(-INFINITY);
         }
     }
 }
@@ -247,36 +155,21 @@ __device__ __forceinline__ float score_error(int score, float s, float p, float 
     return (score == KOSMOS_SCORE_SIGMOID ? 5e-7f : 3e-7f / z + 5e-6f * p) + 1.2e-7f * fabsf(s);
 }
 
-// The groups that stay open, as a bit mask, from the row's values s (closed
-// experts -inf).  The values pass through shared memory, where 32 / G lanes
-// (G rounded up to a power of two) take a group; its stride gsp is the lanes'
-// number modulo 32, so that no two lanes meet in a bank.  err > 0: the error of
-// the values of one group's score; near then tells that the border lies
-// between group scores that their errors do not separate.
-template <int V, int W>
-__device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const float *s, float *s_row, int lane,
-                                                float err, bool &near) {
-    __syncwarp();
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = expert_of<V, W>(lane, v);
-        if (e < p.E) s_row[e + ((e * p.gmul) >> 20) * (p.gsp - p.gs)] = s[v];
-    }
-    __syncwarp();
-    const int g = lane >> p.lp_log2, sub = lane & ((1 << p.lp_log2) - 1);
-    float t1 = -INFINITY, t2 = -INFINITY;
-    if (g < p.G)
-        for (int i = sub; i < p.gs; i += 1 << p.lp_log2) {
-            const float v = s_row[g * p.gsp + i];
-            t2 = fmaxf(t2, fminf(t1, v));
-            t1 = fmaxf(t1, v);
-        }
-    for (int d = 1; d < (1 << p.lp_log2); d <<= 1) {
+// (t1, t2): a lane's best two values; afterwards those of its 1 << n lanes.
+__device__ __forceinline__ void join_top2(float &t1, float &t2, int n) {
+    for (int d = 1; d < (1 << n); d <<= 1) {
         const float o1 = __shfl_xor_sync(FULL, t1, d), o2 = __shfl_xor_sync(FULL, t2, d);
         t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
         t1 = fmaxf(t1, o1);
     }
-    float ge = err + 2.4e-7f * fabsf(t1);  // on the group's score: two scores' errors and their sum's
+}
+
+// Whether this lane's group, group lane >> lp_log2 with best values (t1, t2),
+// stays open.  err > 0: the error of the values behind a group's score; near
+// then tells that the border lies between scores that it does not separate.
+__device__ __forceinline__ bool group_open(const RouteParams &p, float t1, float t2, int lane, float err, bool &near) {
+    const int g = lane >> p.lp_log2;
+    float ge = err + 2.4e-7f * fabsf(t1);  // two scores' errors and their sum's
     if (p.group_top == 2 && t2 != -INFINITY) {
         ge += 2.4e-7f * fabsf(t2);
         t1 += t2;
@@ -286,30 +179,190 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const floa
         const float v = __shfl_sync(FULL, t1, o << p.lp_log2);
         rank += (v > t1 || (v == t1 && o < g)) ? 1 : 0;
     }
-    const bool in = g < p.G && rank < p.GK, out = g < p.G && rank >= p.GK;
+    const bool in = g < p.G && rank < p.GK;
     if (err > 0.f) {
-        float lo = in ? t1 - ge : INFINITY, hi = out && t1 != -INFINITY ? t1 + ge : -INFINITY;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(FULL, lo, d));
-            hi = fmaxf(hi, __shfl_xor_sync(FULL, hi, d));
-        }
-        near = hi != -INFINITY && !(lo > hi);
+        // by keys: the least of the open groups' lower bounds and the largest of the others' upper bounds
+        const uint32_t lo = __reduce_min_sync(FULL, in ? float_key(t1 - ge) : 0xFFFFFFFFu);
+        const uint32_t hi = __reduce_max_sync(FULL, !in && g < p.G && t1 != -INFINITY ? float_key(t1 + ge) : KEY_NONE);
+        near = hi != KEY_NONE && lo <= hi;
     }
-    // one bit per group: every group's first lane votes
-    const uint32_t b = __ballot_sync(FULL, in && sub == 0);
-    uint32_t mask = b;
-    if (p.lp_log2 != 0) {
-        mask = 0u;
-        for (int o = 0; o < p.G; ++o) mask |= ((b >> (o << p.lp_log2)) & 1u) << o;
-    }
-    return mask;
+    return in;
 }
 
+// Groups that are no runs of 2^n lanes: the row's values pass through shared
+// memory, where 1 << lp_log2 lanes take a group; its stride gsp is that number
+// modulo 32, so that no two lanes meet in a bank.
+template <int V>
+__device__ __forceinline__ void group_top2(const RouteParams &p, const float *s, float *s_row, int lane, float &t1,
+                                           float &t2) {
+    __syncwarp();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = expert_of<V>(lane, v);
+        if (e < p.E) s_row[e + ((e * p.gmul) >> 20) * (p.gsp - p.gs)] = s[v];
+    }
+    __syncwarp();
+    const int g = lane >> p.lp_log2;
+    t1 = t2 = -INFINITY;
+    if (g < p.G)
+        for (int i = lane & ((1 << p.lp_log2) - 1); i < p.gs; i += 1 << p.lp_log2) {
+            const float v = s_row[g * p.gsp + i];
+            t2 = fmaxf(t2, fminf(t1, v));
+            t1 = fmaxf(t1, v);
+        }
+    join_top2(t1, t2, p.lp_log2);
+}
+
+// A lane's best two keys that come after (best, be) in the order (key
+// descending, expert ascending), as values v.
+template <typename Key, int V, bool UNIQUE>
+__device__ __forceinline__ void best_two(const Key *key, int lane, Key best, int be, Key &k1, int &v1, Key &k2, int &v2) {
+    k1 = k2 = 0;
+    v1 = v2 = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const Key k = key[v] < best || (!UNIQUE && key[v] == best && expert_of<V>(lane, v) > be) ? key[v] : 0;
+        if (k > k1) { k2 = k1; v2 = v1; k1 = k; v1 = v; }
+        else if (k > k2) { k2 = k; v2 = v; }
+    }
+}
+
+__device__ __forceinline__ uint32_t warp_max_key(uint32_t k) { return __reduce_max_sync(FULL, k); }
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
+    const uint32_t hi = __reduce_max_sync(FULL, static_cast<uint32_t>(k >> 32));
+    const uint32_t lo = __reduce_max_sync(FULL, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// The row's experts in their order, one per call of next(): a warp-wide
+// maximum over every lane's best two keys; a lane that has given both away
+// looks for its next two.  UNIQUE: keys differ and hold the expert in their
+// low bits; otherwise ties go to the lowest lane, which holds the lowest expert.
+template <typename Key, int V, bool UNIQUE> struct Chooser {
+    const Key *key;
+    int lane, have = 2;
+    Key k1, k2;
+    int v1, v2;
+    Key best = 0;
+    int e = 0;
+
+    __device__ __forceinline__ Chooser(const Key *k, int l) : key(k), lane(l) { restart(); }
+    __device__ __forceinline__ void restart() {
+        best_two<Key, V, true>(key, lane, ~static_cast<Key>(0), -1, k1, v1, k2, v2);
+    }
+    __device__ __forceinline__ void next() {
+        best = warp_max_key(k1);
+        bool won = k1 == best;
+        if (UNIQUE) {
+            e = static_cast<int>(LOW13 - (best & LOW13));
+        } else {
+            const int src = __ffs(__ballot_sync(FULL, won)) - 1;
+            e = __shfl_sync(FULL, expert_of<V>(lane, v1), src);
+            won = lane == src;
+        }
+        if (won) { k1 = k2; v1 = v2; --have; }
+        if (__any_sync(FULL, have == 0)) {
+            if (have == 0) {
+                best_two<Key, V, UNIQUE>(key, lane, best, e, k1, v1, k2, v2);
+                have = 2;
+            }
+        }
+    }
+};
+
+// 64-bit keys, ordered like the doubles; NaN and -inf are closed.
+constexpr uint64_t KEY64_CLOSED = 0x000FFFFFFFFFFFFFull;
+__device__ __forceinline__ uint64_t double_key(double s) {
+    if (!(s > -INFINITY)) return KEY64_CLOSED;
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(s + 0.0));
+    return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double key_double(uint64_t k) {
+    return __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
+}
+
+// Chooses the row's experts by their 64-bit selection scores; lane j < k gets
+// the j-th expert and whether it is open.  Comparisons are of integer keys:
+// fp64 instructions are rare here (two lanes a cycle) and a row in this
+// function is waited for.
+template <typename T, int V>
+__device__ __noinline__ void choose_f64(const RouteParams &p, const T *row, int lane, int &my_e, bool &my_open) {
+    alignas(16) T raw[V];
+    load_row<T, V>(row, p.E, lane, p.vec, raw);
+    const bool by_logit = p.bias == nullptr;
+    double m = 0.0, z = 1.0;
+    if (p.score == KOSMOS_SCORE_SOFTMAX) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) top = fmaxf(top, to_f32(raw[v]));
+        m = key_float(__reduce_max_sync(FULL, float_key(top)));
+        z = 0.0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (to_f32(raw[v]) > -INFINITY) z += exp(static_cast<double>(to_f32(raw[v])) - m);
+        z = warp_sum(z);
+    }
+    uint64_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = expert_of<V>(lane, v);
+        const double x = to_f32(raw[v]);
+        key[v] = KEY64_CLOSED;
+        if (x > -INFINITY) {
+            double s = p.score == KOSMOS_SCORE_SOFTMAX ? exp(x - m) / z : 1.0 / (1.0 + exp(-x));
+            if (!by_logit) s += static_cast<double>(p.bias[e]);
+            key[v] = double_key(s);
+        }
+    }
+    if (p.GK < p.G) {
+        double score = -INFINITY;  // lane g: the score of group g
+        for (int g = 0; g < p.G; ++g) {
+            // the group's best two keys: the best two of every lane, then of the warp
+            uint64_t k1 = 0, k2 = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = expert_of<V>(lane, v) - g * (p.E / p.G);
+                const uint64_t k = e >= 0 && e < p.E / p.G ? key[v] : 0;
+                if (k > k1) { k2 = k1; k1 = k; }
+                else if (k > k2) k2 = k;
+            }
+            const uint64_t b1 = warp_max_key(k1);
+            const int src = __ffs(__ballot_sync(FULL, k1 == b1)) - 1;
+            const uint64_t b2 = warp_max_key(lane == src ? k2 : k1);
+            double t = key_double(b1);
+            if (p.group_top == 2 && b2 > KEY64_CLOSED) t += key_double(b2);
+            if (lane == g) score = t;
+        }
+        int rank = 0;
+        const uint64_t mine = double_key(score);
+        for (int g = 0; g < p.G; ++g) {
+            const uint64_t o = __shfl_sync(FULL, mine, g);
+            rank += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+        }
+        const uint32_t open = __ballot_sync(FULL, lane < p.G && rank < p.GK);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = expert_of<V>(lane, v);
+            if (e < p.E && !((open >> (e / (p.E / p.G))) & 1u)) key[v] = KEY64_CLOSED;
+        }
+    }
+    if (by_logit) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (key[v] > KEY64_CLOSED) key[v] = double_key(static_cast<double>(to_f32(raw[v])));
+    }
+    Chooser<uint64_t, V, false> c(key, lane);
+    for (int j = 0; j < p.k; ++j) {
+        c.next();
+        if (lane == j) { my_e = c.e; my_open = c.best > KEY64_CLOSED; }
+    }
+}
+
+// A warp takes p.rows consecutive rows at a time (slots lanes each, a power of
+// two): the rows are ordered one after the other, and their gates are then
+// computed together, lane r * slots + j holding row r's j-th choice.
 template <typename T, int V, int MODE>
-__global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(const __grid_constant__ RouteParams p) {
-    constexpr int WMAX = 16 / static_cast<int>(sizeof(T));
-    constexpr int W = V < WMAX ? V : WMAX;
+__global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel(const __grid_constant__ RouteParams p) {
     extern __shared__ int32_t s_mem[];
     int32_t *s_hist = s_mem;                                           // [E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -319,132 +372,186 @@ __global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(const __grid_const
         __syncthreads();
     }
     const bool by_logit = MODE != BY_SCORE || p.bias == nullptr;
-    const bool softmax = p.score == KOSMOS_SCORE_SOFTMAX;
+    const bool softmax = p.score == KOSMOS_SCORE_SOFTMAX, groups = p.GK < p.G;
     const bool need_z = softmax && (MODE == BY_SCORE || !p.renorm);
-    const int rounds = p.k + ((MODE == BY_SCORE && !by_logit && p.k < p.E) ? 1 : 0);  // one more: the border's other side
     float bias[V];
     if (MODE == BY_SCORE) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = expert_of<V, W>(lane, v);
+            const int e = expert_of<V>(lane, v);
             bias[v] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.f;
         }
     }
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * ROUTE_WARPS + warp; t < p.T;
-         t += static_cast<int64_t>(gridDim.x) * ROUTE_WARPS) {
-        const T *row = static_cast<const T *>(p.logits) + t * p.ld;
-        float x[V];
-        load_row<T, V, W>(row, p.E, lane, p.vec, x);
-        bool nan = false;
-        float m = -INFINITY, z = 1.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            nan = nan || x[v] != x[v] || (softmax && x[v] == INFINITY);
-            m = fmaxf(m, x[v]);  // skips NaN
-        }
-        nan = __any_sync(FULL, nan);
-        if (need_z) {
-            m = warp_max(m);
-            z = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) z += x[v] > -INFINITY ? __expf(x[v] - m) : 0.f;
-            z = warp_sum(z);
-        }
-        // the row's order: s, closed experts -inf
-        float s[V];
-        bool near = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            s[v] = x[v];
-            if (MODE == BY_SCORE && !(by_logit && p.GK == p.G)) {
-                s[v] = softmax ? __fdividef(__expf(x[v] - m), z) : __fdividef(1.0f, 1.0f + __expf(-x[v]));
-                s[v] = x[v] > -INFINITY ? s[v] + bias[v] : -INFINITY;
-            }
-            s[v] = s[v] > -INFINITY ? s[v] : -INFINITY;  // NaN
-        }
-        uint32_t open = FULL;
-        if (p.GK < p.G) {
-            const float err = MODE == BY_SCORE ? p.group_top * (softmax ? 5.3e-6f / z : 5e-7f) : 0.f;
-            open = open_groups<V, W>(p, s, s_row, lane, err, near);
-        }
-        uint32_t key[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = expert_of<V, W>(lane, v);
-            float o = MODE == BY_SCORE && by_logit && s[v] > -INFINITY ? x[v] : s[v];
-            if (p.GK < p.G && !((open >> ((e * p.gmul) >> 20)) & 1u)) o = -INFINITY;
-            key[v] = float_key(o);
-            if (MODE == BY_LOGIT16) key[v] = (key[v] & ~LOW13) | (LOW13 - e);
-            if (e >= p.E) key[v] = KEY_NONE;
-        }
-        // k rounds of a warp-wide maximum over every lane's best two; a lane
-        // that has given both away looks for its next two
-        uint32_t my_key = KEY_NONE;
+    const T *logits = static_cast<const T *>(p.logits);
+    const int seg = lane / p.slots, slot = lane % p.slots;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * ROUTE_WARPS * p.rows;
+    int64_t t0 = (static_cast<int64_t>(blockIdx.x) * ROUTE_WARPS + warp) * p.rows;
+    alignas(16) T next[V];
+    if (t0 < p.T) load_row<T, V>(logits + t0 * p.ld, p.E, lane, p.vec, next);
+    for (; t0 < p.T; t0 += stride) {
+        uint32_t my_key = KEY_NONE, border = KEY_NONE;
         int my_e = 0;
-        uint32_t k1 = KEY_NONE, k2 = KEY_NONE;
-        int e1 = 0x7FFFFFFF, e2 = 0x7FFFFFFF, have = 2;
+        float my_m = 0.f, my_z = 1.f;
+        bool my_nan = false, my_near = false;
+        const int rows = p.T - t0 < p.rows ? static_cast<int>(p.T - t0) : p.rows;
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r) {
+            float x[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = expert_of<V, W>(lane, v);
-            if (key[v] > k1) { k2 = k1; e2 = e1; k1 = key[v]; e1 = e; }
-            else if (key[v] > k2) { k2 = key[v]; e2 = e; }
-        }
-        for (int j = 0; j < rounds; ++j) {
-            const uint32_t best = __reduce_max_sync(FULL, k1);
-            int e = e1;
-            if (MODE != BY_LOGIT16) e = __reduce_min_sync(FULL, k1 == best ? static_cast<uint32_t>(e1) : 0x7FFFFFFFu);
-            const bool won = k1 == best && (MODE == BY_LOGIT16 || e == e1);
-            if (lane == j) { my_key = best; my_e = e; }
-            if (won) { k1 = k2; e1 = e2; --have; }
-            if (__any_sync(FULL, have == 0) && j + 1 < rounds) {
-                if (have == 0) {
-                    k1 = k2 = KEY_NONE;
-                    e1 = e2 = 0x7FFFFFFF;
-                    have = 2;
+            for (int v = 0; v < V; ++v) x[v] = to_f32(next[v]);
+            const int64_t tn = r + 1 < rows ? t0 + r + 1 : t0 + stride;
+            if (tn < p.T) load_row<T, V>(logits + tn * p.ld, p.E, lane, p.vec, next);
+            bool nan = false;
+            float m = -INFINITY, z = 1.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                nan = nan || x[v] != x[v];
+                x[v] = fmaxf(x[v], -INFINITY);  // NaN: closed
+            }
+            if (softmax) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
+                nan = nan || m == INFINITY;
+            }
+            nan = __any_sync(FULL, nan);
+            if (need_z) {
+                m = key_float(__reduce_max_sync(FULL, float_key(m)));
+                z = 0.f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) z += x[v] > -INFINITY ? __expf(x[v] - m) : 0.f;
+                z = warp_sum(z);
+            }
+            // s: what groups are scored by, and without by_logit what orders
+            // the experts; closed experts -inf
+            float s[V];
+            uint32_t key[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[v] = x[v];
+                if (MODE == BY_SCORE) {
+                    const float q = softmax ? __fdividef(__expf(x[v] - m), z) : __fdividef(1.0f, 1.0f + __expf(-x[v]));
+                    s[v] = x[v] > -INFINITY ? fmaxf(q + bias[v], -INFINITY) : -INFINITY;
+                }
+                key[v] = float_key(MODE == BY_SCORE && by_logit ? x[v] : s[v]);
+                if (MODE == BY_LOGIT16) key[v] = (key[v] & ~LOW13) | (LOW13 - expert_of<V>(lane, v));
+            }
+            Chooser<uint32_t, V, MODE == BY_LOGIT16> c(key, lane);
+            bool near = false;
+            if (groups) {
+                const float err = MODE == BY_SCORE ? p.group_top * (softmax ? 5.3e-6f / z : 5e-7f) : 0.f;
+                float t1, t2;
+                if (p.lane_groups) {
+                    if (MODE == BY_SCORE && by_logit) {
+                        t1 = t2 = -INFINITY;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            t2 = fmaxf(t2, fminf(t1, s[v]));
+                            t1 = fmaxf(t1, s[v]);
+                        }
+                    } else if (MODE == BY_LOGIT16) {  // one value per group counts here
+                        t1 = key_float((c.k1 & 0x80000000u) ? c.k1 & ~LOW13 : c.k1 | LOW13);
+                        t2 = -INFINITY;
+                    } else {
+                        t1 = key_float(c.k1);
+                        t2 = key_float(c.k2);
+                    }
+                    join_top2(t1, t2, p.lp_log2);
+                    if (!group_open(p, t1, t2, lane, err, near)) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            key[v] = MODE == BY_LOGIT16 ? (KEY_CLOSED & ~LOW13) | (LOW13 - expert_of<V>(lane, v)) : KEY_CLOSED;
+                        c.k1 = key[0]; c.v1 = 0;
+                        c.k2 = key[1]; c.v2 = 1;
+                    }
+                } else {
+                    group_top2<V>(p, s, s_row, lane, t1, t2);
+                    const uint32_t open = __ballot_sync(FULL, group_open(p, t1, t2, lane, err, near));
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        const int ev = expert_of<V, W>(lane, v);
-                        const bool left = key[v] < best || (MODE != BY_LOGIT16 && key[v] == best && ev > e);
-                        if (left && key[v] > k1) { k2 = k1; e2 = e1; k1 = key[v]; e1 = ev; }
-                        else if (left && key[v] > k2) { k2 = key[v]; e2 = ev; }
+                        const int e = expert_of<V>(lane, v);
+                        const int g = e < p.E ? (e * p.gmul) >> 20 : 0;
+                        if (!((open >> (g << p.lp_log2)) & 1u))
+                            key[v] = MODE == BY_LOGIT16 ? (KEY_CLOSED & ~LOW13) | (LOW13 - e) : KEY_CLOSED;
                     }
+                    c.restart();
                 }
             }
+#pragma unroll 1
+            for (int j = 0; j < p.k; ++j) {
+                c.next();
+                if (lane == r * p.slots + j) { my_key = c.best; my_e = c.e; }
+            }
+            if (MODE == BY_SCORE && !by_logit && p.k < p.E) {
+                // the border's other side: the first that is no tie, in 64 bits too, of the last one chosen
+                const uint32_t last = c.best;
+                const int le = c.e;
+                c.next();
+                for (int n = p.k + 1; c.best == last && last > KEY_CLOSED; ++n) {
+                    const T *row = logits + (t0 + r) * p.ld;
+                    if (to_f32(row[c.e]) != to_f32(row[le]) || p.bias[c.e] != p.bias[le]) { near = true; break; }
+                    if (n >= p.E) { c.best = KEY_NONE; break; }
+                    c.next();
+                }
+            }
+            if (seg == r) {
+                border = c.best;
+                my_nan = nan;
+                my_near = near;
+                my_m = m;
+                my_z = z;
+            }
         }
-        const bool mine = lane < p.k;
+        // ---- the rows together
+        const bool mine = seg < rows && slot < p.k;
+        const T *row = logits + (t0 + (seg < rows ? seg : 0)) * p.ld;
         bool my_open;
         float my_x = 0.f;
         if (MODE == BY_LOGIT16) {
-            my_e = LOW13 - (my_key & LOW13);
             my_open = (my_key | LOW13) > KEY_CLOSED;
             my_x = key_float((my_key & 0x80000000u) ? my_key & ~LOW13 : my_key | LOW13);
         } else {
             my_open = my_key > KEY_CLOSED;
-            if (MODE == BY_LOGIT32) my_x = key_float(my_key);
+            my_x = MODE == BY_LOGIT32 ? key_float(my_key) : mine ? to_f32(row[my_e]) : 0.f;
         }
         if (MODE == BY_SCORE) {
-            if (lane < rounds) my_x = to_f32(row[my_e]);
             if (!by_logit) {
                 // neighbours closer than their errors, unless they are the same logit
                 // and bias (a tie in 64 bits too, which the index has broken)
-                const float my_s = key_float(my_key), my_b = lane < rounds ? p.bias[my_e] : 0.f;
-                const float my_err = score_error(p.score, my_s, fabsf(my_s - my_b), z);
-                const float s2 = __shfl_down_sync(FULL, my_s, 1), err2 = __shfl_down_sync(FULL, my_err, 1);
+                const float my_s = key_float(my_key), my_b = mine ? p.bias[my_e] : 0.f;
+                const float my_err = score_error(p.score, my_s, fabsf(my_s - my_b), my_z);
+                float s2 = __shfl_down_sync(FULL, my_s, 1), err2 = __shfl_down_sync(FULL, my_err, 1);
                 const float x2 = __shfl_down_sync(FULL, my_x, 1), b2 = __shfl_down_sync(FULL, my_b, 1);
-                const bool open2 = __shfl_down_sync(FULL, static_cast<int>(my_open), 1) != 0;
-                near = near || (lane + 1 < rounds && my_open && open2 && !(my_s - s2 > my_err + err2) &&
-                                !(my_x == x2 && my_b == b2));
+                bool open2 = __shfl_down_sync(FULL, static_cast<int>(my_open), 1) != 0;
+                bool tie = my_x == x2 && my_b == b2;
+                if (slot == p.k - 1) {
+                    s2 = key_float(border);
+                    open2 = border > KEY_CLOSED;
+                    tie = false;
+                    // the border's own error: its p is at most the chosen one's s less the least bias; bounded by p = 1
+                    err2 = score_error(p.score, s2, p.score == KOSMOS_SCORE_SIGMOID ? 0.f : 1.0f / my_z, my_z);
+                }
+                my_near = my_near || (my_open && open2 && !(my_s - s2 > my_err + err2) && !tie);
+                my_near = my_near && mine;
             }
-            if (__any_sync(FULL, near)) {
-                choose_f64<T, V, W>(p, row, lane, my_e, my_open);
+            const uint32_t nb = __ballot_sync(FULL, my_near && seg < rows);
+            if (nb != 0u) {
+                for (int r = 0; r < rows; ++r) {
+                    if (((nb >> (r * p.slots)) & (p.slots == 32 ? FULL : (1u << p.slots) - 1u)) == 0u) continue;
+                    int ce = 0;
+                    bool co = false;
+                    choose_f64<T, V>(p, logits + (t0 + r) * p.ld, lane, ce, co);
+                    ce = __shfl_sync(FULL, ce, slot);
+                    const int coi = __shfl_sync(FULL, static_cast<int>(co), slot);
+                    if (seg == r) { my_e = ce; my_open = coi != 0; }
+                }
                 if (mine) my_x = to_f32(row[my_e]);
             }
         }
-        float g = route_gate(p, my_x, mine && my_open, m, z);
-        if (nan) g = NAN;
+        float g = route_gate(p, my_x, mine && my_open, my_m, my_z);
+        if (my_nan) g = NAN;
         if (mine) {
-            p.idx[t * p.k + lane] = my_e;
-            p.gate[t * p.k + lane] = g;
+            p.idx[(t0 + seg) * p.k + slot] = my_e;
+            p.gate[(t0 + seg) * p.k + slot] = g;
             if (p.counts != nullptr) atomicAdd(&s_hist[my_e], 1);
         }
     }
@@ -474,22 +581,32 @@ __global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(const __grid_const
 
 template <typename T, int MODE> kosmos_status launch_route_m(const RouteParams &q, int sms, cudaStream_t stream) {
     RouteParams p = q;
-    int64_t blocks = cdiv(p.T, ROUTE_WARPS);
-    if (blocks > 4ll * sms) blocks = 4ll * sms;
-    const dim3 grid(static_cast<unsigned>(blocks));
     const int v = p.E <= 64 ? 2 : p.E <= 128 ? 4 : p.E <= 256 ? 8 : p.E <= 512 ? 16 : 32;
-    const int w = v < 16 / static_cast<int>(sizeof(T)) ? v : 16 / static_cast<int>(sizeof(T));
-    const int64_t run = w * static_cast<int64_t>(sizeof(T));
-    p.vec = p.E % w == 0 && reinterpret_cast<uintptr_t>(p.logits) % run == 0 && p.ld * sizeof(T) % run == 0;
+    const int es = static_cast<int>(sizeof(T));
+    const int w = v * es < 16 ? v : 16 / es;  // values per load
+    p.vec = p.E % w == 0 && reinterpret_cast<uintptr_t>(p.logits) % (w * es) == 0 && p.ld * es % (w * es) == 0;
+    // several rows per warp share the gates' arithmetic, once every warp has
+    // some; before that a row's latency counts
+    p.slots = p.k <= 8 ? 8 : 16;
+    p.rows = p.T >= ROUTE_ROWS_FROM * static_cast<int64_t>(sms) ? 32 / p.slots : 1;
+    int64_t blocks = cdiv(p.T, ROUTE_WARPS * p.rows);
+    if (blocks > MINB * static_cast<int64_t>(sms)) blocks = MINB * static_cast<int64_t>(sms);
+    const dim3 grid(static_cast<unsigned>(blocks));
     p.hist_words = p.counts != nullptr ? p.E : 0;
     p.row_words = 0;
+    p.lane_groups = false;
     if (p.GK < p.G) {
         p.gs = p.E / p.G;
-        p.gmul = ((1 << 20) + p.gs - 1) / p.gs;  // e * gmul >> 20 = e / gs for e < 1024
+        p.lane_groups = p.gs % v == 0 && (p.gs / v & (p.gs / v - 1)) == 0;
         p.lp_log2 = 0;
-        while ((p.G << (p.lp_log2 + 1)) <= 32) ++p.lp_log2;
-        p.gsp = p.gs + ((1 << p.lp_log2) - p.gs % 32 + 32) % 32;
-        p.row_words = p.G * p.gsp;
+        if (p.lane_groups) {
+            while (v << p.lp_log2 < p.gs) ++p.lp_log2;
+        } else {
+            p.gmul = ((1 << 20) + p.gs - 1) / p.gs;  // e * gmul >> 20 = e / gs for e < 1024
+            while ((p.G << (p.lp_log2 + 1)) <= 32) ++p.lp_log2;
+            p.gsp = p.gs + ((1 << p.lp_log2) - p.gs % 32 + 32) % 32;
+            p.row_words = p.G * p.gsp;
+        }
     }
     const size_t smem = 4ull * (p.hist_words + ROUTE_WARPS * p.row_words);
     switch (v) {
