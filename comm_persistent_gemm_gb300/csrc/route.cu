@@ -4,9 +4,9 @@
 // stay open, renormalised and scaled gates, tokens per expert), and the
 // gradient of the gates with respect to the logits.
 //
-// One warp per token; lane l holds V of the row's values.  The choice is k
-// rounds of a warp-wide maximum; what decides it is an order that ties break
-// towards the lower expert, so the result is a function of the row alone.
+// One warp orders a row; lane l holds V consecutive experts of it.  The choice
+// is k rounds of a warp-wide maximum; what decides it is an order in which ties
+// go to the lower expert, so the result is a function of the row alone.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -96,15 +96,11 @@ __device__ __forceinline__ float route_gate(const RouteParams &p, float x, bool 
 }
 
 // ------------------------------------------------------------ fp32 choice
-// How a kernel orders a row's experts:
-//   BY_LOGIT16  without a bias, 16-bit logits: the key holds the logit (19 bits
-//               order a bf16 or fp16 value) and the expert, so keys differ and
-//               one warp-wide maximum finds value and expert together;
-//   BY_LOGIT32  without a bias, fp32 logits: the key is the logit;
-//   BY_SCORE    the fp32 selection score.  Rows in which two neighbours in the
-//               order, or the groups either side of the border, are closer
-//               than the scores' rounding error are chosen again in 64 bits.
-enum RouteMode : int { BY_LOGIT16 = 0, BY_LOGIT32 = 1, BY_SCORE = 2 };
+// How a kernel orders a row's experts: without a bias by their logits, which
+// the scores rise with; else by s = p + bias in fp32.  Rows in which two
+// neighbours in the order, or the groups either side of the border, are closer
+// than the scores' rounding error are chosen again in 64 bits.
+enum RouteMode : int { BY_LOGIT = 0, BY_SIGMOID = 1, BY_SOFTMAX = 2 };
 
 // Order-preserving map of floats to unsigned integers (-0 as +0).  Closed
 // experts have the key of -inf, and so have the places beyond E, which
@@ -145,14 +141,34 @@ __device__ __forceinline__ void load_row(const T *row, int E, int lane, bool vec
     }
 }
 
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// p in fp32 (rz = 1 / z): x = -inf gives 0.
+template <int MODE> __device__ __forceinline__ float fast_p(float x, float m, float rz) {
+    if (MODE == BY_SIGMOID) return rcp(1.0f + ex2(-LOG2E * x));
+    return ex2(LOG2E * (x - m)) * rz;
+}
+
 // Bounds on the distance between an fp32 score and the 64-bit one.  Sigmoid:
-// the fast exponential is off by 2 + 1.2 |x| steps, which p (1 - p) brings
-// under 6e-8; sum and division 3e-7 p; the bias' addition 6e-8 |s|.  Softmax:
-// e^-y of a term y below the maximum is off by (2.5 + 1.7 y) steps, at most 3e-7
-// of the largest term; the row's sum by 5e-6 (its terms' errors weigh
-// at most ln 1024, and 37 additions); the bias as above.
-__device__ __forceinline__ float score_error(int score, float s, float p, float z) {
-    return (score == KOSMOS_SCORE_SIGMOID ? 5e-7f : 3e-7f / z + 5e-6f * p) + 1.2e-7f * fabsf(s);
+// the exponential is off by 2 + 1.2 |x| steps of 2^-23 (argument and result),
+// which p (1 - p) brings under 6e-8; sum and reciprocal 3e-7 p; the bias'
+// addition 6e-8 |s|.  Softmax: e^-y of a term y below the maximum is off by
+// (2.5 + 1.7 y) steps, at most 3e-7 of the largest term; the row's sum and its
+// reciprocal by 5e-6 (its terms' errors weigh at most ln 1024, and there are 37
+// additions); the bias as above.
+template <int MODE> __device__ __forceinline__ float score_error(float s, float p, float rz) {
+    if (MODE == BY_LOGIT) return 0.f;
+    return (MODE == BY_SIGMOID ? 5e-7f : 3e-7f * rz + 5e-6f * p) + 1.2e-7f * fabsf(s);
 }
 
 // (t1, t2): a lane's best two values; afterwards those of its 1 << n lanes.
@@ -174,11 +190,15 @@ __device__ __forceinline__ bool group_open(const RouteParams &p, float t1, float
         ge += 2.4e-7f * fabsf(t2);
         t1 += t2;
     }
+    // a group's lanes share the comparison with the others
     int rank = 0;
-    for (int o = 0; o < p.G; ++o) {
+    const int lp = 1 << p.lp_log2;
+    for (int o0 = 0; o0 < p.G; o0 += lp) {
+        const int o = o0 + (lane & (lp - 1));
         const float v = __shfl_sync(FULL, t1, o << p.lp_log2);
-        rank += (v > t1 || (v == t1 && o < g)) ? 1 : 0;
+        rank += o < p.G && (v > t1 || (v == t1 && o < g)) ? 1 : 0;
     }
+    for (int d = 1; d < lp; d <<= 1) rank += __shfl_xor_sync(FULL, rank, d);
     const bool in = g < p.G && rank < p.GK;
     if (err > 0.f) {
         // by keys: the least of the open groups' lower bounds and the largest of the others' upper bounds
@@ -213,62 +233,90 @@ __device__ __forceinline__ void group_top2(const RouteParams &p, const float *s,
     join_top2(t1, t2, p.lp_log2);
 }
 
-// A lane's best two keys that come after (best, be) in the order (key
-// descending, expert ascending), as values v.
-template <typename Key, int V, bool UNIQUE>
-__device__ __forceinline__ void best_two(const Key *key, int lane, Key best, int be, Key &k1, int &v1, Key &k2, int &v2) {
-    k1 = k2 = 0;
-    v1 = v2 = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const Key k = key[v] < best || (!UNIQUE && key[v] == best && expert_of<V>(lane, v) > be) ? key[v] : 0;
-        if (k > k1) { k2 = k1; v2 = v1; k1 = k; v1 = v; }
-        else if (k > k2) { k2 = k; v2 = v; }
-    }
-}
+// The row's experts in their order, one per call of next(): a warp-wide
+// maximum over the lanes' lists of their best D values; a lane that has given
+// its list away makes the next one.  A key's low bits tell a lane's values
+// apart.  UNIQUE (16-bit logits, whose order takes 19 bits): they hold the expert,
+// so the maximum tells which one it is.  Otherwise they hold V - 1 - v, the
+// order of values is that without the low bits, and of equal ones the
+// lowest lane, which holds the lower experts, comes first.
+template <int V, bool UNIQUE> struct Chooser {
+    static constexpr int D = V <= 4 ? V : V == 8 ? 4 : 2;
+    static constexpr uint32_t MASK = UNIQUE ? LOW13 : V - 1;
+    const uint32_t *key;
+    int lane;
+    uint32_t k[D];
+    uint32_t best = KEY_NONE;  // value (low bits set unless UNIQUE) and expert of the last call
+    int e = 0;
 
-__device__ __forceinline__ uint32_t warp_max_key(uint32_t k) { return __reduce_max_sync(FULL, k); }
+    static __device__ __forceinline__ uint32_t key_of(float f, int lane, int v) {
+        return (float_key(f) & ~MASK) | (MASK - (UNIQUE ? expert_of<V>(lane, v) : v));
+    }
+    __device__ __forceinline__ Chooser(const uint32_t *keys, int l) : key(keys), lane(l) { list(~0u); }
+    // the largest D keys below limit
+    __device__ __forceinline__ void list(uint32_t limit) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) k[d] = KEY_NONE;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            uint32_t x = key[v] < limit ? key[v] : KEY_NONE;
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const uint32_t hi = max(k[d], x);
+                x = min(k[d], x);
+                k[d] = hi;
+            }
+        }
+    }
+    __device__ __forceinline__ void next() {
+        const uint32_t given = k[0];
+        bool won;
+        if (UNIQUE) {
+            best = __reduce_max_sync(FULL, k[0]);
+            e = static_cast<int>(MASK - (best & MASK));
+            won = k[0] == best;
+        } else {
+            best = __reduce_max_sync(FULL, k[0] | MASK);
+            const int src = __ffs(__ballot_sync(FULL, (k[0] | MASK) == best)) - 1;
+            e = expert_of<V>(src, static_cast<int>(MASK - (__shfl_sync(FULL, k[0], src) & MASK)));
+            won = lane == src;
+        }
+        if (won) {
+#pragma unroll
+            for (int d = 0; d + 1 < D; ++d) k[d] = k[d + 1];
+            k[D - 1] = KEY_NONE;
+        }
+        if (D < V && __any_sync(FULL, k[0] == KEY_NONE)) {
+            if (k[0] == KEY_NONE) list(given);
+        }
+    }
+};
+
+// The same for the rows that are ordered by 64-bit keys: ties are exact ones.
+struct Best64 {
+    uint64_t key;
+    int e;
+};
 __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
     const uint32_t hi = __reduce_max_sync(FULL, static_cast<uint32_t>(k >> 32));
     const uint32_t lo = __reduce_max_sync(FULL, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
     return static_cast<uint64_t>(hi) << 32 | lo;
 }
-
-// The row's experts in their order, one per call of next(): a warp-wide
-// maximum over every lane's best two keys; a lane that has given both away
-// looks for its next two.  UNIQUE: keys differ and hold the expert in their
-// low bits; otherwise ties go to the lowest lane, which holds the lowest expert.
-template <typename Key, int V, bool UNIQUE> struct Chooser {
-    const Key *key;
-    int lane, have = 2;
-    Key k1, k2;
-    int v1, v2;
-    Key best = 0;
-    int e = 0;
-
-    __device__ __forceinline__ Chooser(const Key *k, int l) : key(k), lane(l) { restart(); }
-    __device__ __forceinline__ void restart() {
-        best_two<Key, V, true>(key, lane, ~static_cast<Key>(0), -1, k1, v1, k2, v2);
-    }
-    __device__ __forceinline__ void next() {
-        best = warp_max_key(k1);
-        bool won = k1 == best;
-        if (UNIQUE) {
-            e = static_cast<int>(LOW13 - (best & LOW13));
-        } else {
-            const int src = __ffs(__ballot_sync(FULL, won)) - 1;
-            e = __shfl_sync(FULL, expert_of<V>(lane, v1), src);
-            won = lane == src;
-        }
-        if (won) { k1 = k2; v1 = v2; --have; }
-        if (__any_sync(FULL, have == 0)) {
-            if (have == 0) {
-                best_two<Key, V, UNIQUE>(key, lane, best, e, k1, v1, k2, v2);
-                have = 2;
-            }
-        }
-    }
-};
+template <int V> __device__ __forceinline__ Best64 take_best64(uint64_t *key, int lane) {
+    uint64_t k = 0;
+    int at = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (key[v] > k) { k = key[v]; at = v; }
+    Best64 b;
+    b.key = warp_max_key(k);
+    const int src = __ffs(__ballot_sync(FULL, k == b.key)) - 1;
+    b.e = __shfl_sync(FULL, expert_of<V>(lane, at), src);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (b.e == expert_of<V>(lane, v)) key[v] = 0;
+    return b;
+}
 
 // 64-bit keys, ordered like the doubles; NaN and -inf are closed.
 constexpr uint64_t KEY64_CLOSED = 0x000FFFFFFFFFFFFFull;
@@ -351,10 +399,9 @@ __device__ __noinline__ void choose_f64(const RouteParams &p, const T *row, int 
         for (int v = 0; v < V; ++v)
             if (key[v] > KEY64_CLOSED) key[v] = double_key(static_cast<double>(to_f32(raw[v])));
     }
-    Chooser<uint64_t, V, false> c(key, lane);
     for (int j = 0; j < p.k; ++j) {
-        c.next();
-        if (lane == j) { my_e = c.e; my_open = c.best > KEY64_CLOSED; }
+        const Best64 b = take_best64<V>(key, lane);
+        if (lane == j) { my_e = b.e; my_open = b.key > KEY64_CLOSED; }
     }
 }
 
@@ -363,6 +410,9 @@ __device__ __noinline__ void choose_f64(const RouteParams &p, const T *row, int 
 // computed together, lane r * slots + j holding row r's j-th choice.
 template <typename T, int V, int MODE>
 __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel(const __grid_constant__ RouteParams p) {
+    constexpr bool UNIQUE = MODE == BY_LOGIT && sizeof(T) == 2;
+    using Choose = Chooser<V, UNIQUE>;
+    constexpr uint32_t MASK = Choose::MASK;
     extern __shared__ int32_t s_mem[];
     int32_t *s_hist = s_mem;                                           // [E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -371,11 +421,10 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel
         for (int i = threadIdx.x; i < p.E; i += ROUTE_THREADS) s_hist[i] = 0;
         __syncthreads();
     }
-    const bool by_logit = MODE != BY_SCORE || p.bias == nullptr;
-    const bool softmax = p.score == KOSMOS_SCORE_SOFTMAX, groups = p.GK < p.G;
-    const bool need_z = softmax && (MODE == BY_SCORE || !p.renorm);
+    const bool softmax = MODE == BY_SOFTMAX || (MODE == BY_LOGIT && p.score == KOSMOS_SCORE_SOFTMAX);
+    const bool need_z = MODE == BY_SOFTMAX || (softmax && !p.renorm);
     float bias[V];
-    if (MODE == BY_SCORE) {
+    if (MODE != BY_LOGIT) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = expert_of<V>(lane, v);
@@ -406,7 +455,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 nan = nan || x[v] != x[v];
-                x[v] = fmaxf(x[v], -INFINITY);  // NaN: closed
+                if (MODE != BY_SIGMOID) x[v] = fmaxf(x[v], -INFINITY);  // NaN: closed
             }
             if (softmax) {
 #pragma unroll
@@ -414,54 +463,49 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel
                 nan = nan || m == INFINITY;
             }
             nan = __any_sync(FULL, nan);
+            // s: what orders the experts and scores the groups; closed experts -inf
+            float s[V];
             if (need_z) {
                 m = key_float(__reduce_max_sync(FULL, float_key(m)));
+                if (m == -INFINITY) m = 0.f;
                 z = 0.f;
 #pragma unroll
-                for (int v = 0; v < V; ++v) z += x[v] > -INFINITY ? __expf(x[v] - m) : 0.f;
+                for (int v = 0; v < V; ++v) {
+                    s[v] = ex2(LOG2E * (x[v] - m));
+                    z += s[v];
+                }
                 z = warp_sum(z);
             }
-            // s: what groups are scored by, and without by_logit what orders
-            // the experts; closed experts -inf
-            float s[V];
+            const float rz = MODE == BY_SOFTMAX ? rcp(z) : 1.f;
             uint32_t key[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                s[v] = x[v];
-                if (MODE == BY_SCORE) {
-                    const float q = softmax ? __fdividef(__expf(x[v] - m), z) : __fdividef(1.0f, 1.0f + __expf(-x[v]));
+                if (MODE == BY_LOGIT) {
+                    s[v] = x[v];
+                } else {
+                    const float q = MODE == BY_SOFTMAX ? s[v] * rz : fast_p<BY_SIGMOID>(x[v], 0.f, 1.f);
                     s[v] = x[v] > -INFINITY ? fmaxf(q + bias[v], -INFINITY) : -INFINITY;
                 }
-                key[v] = float_key(MODE == BY_SCORE && by_logit ? x[v] : s[v]);
-                if (MODE == BY_LOGIT16) key[v] = (key[v] & ~LOW13) | (LOW13 - expert_of<V>(lane, v));
+                key[v] = Choose::key_of(s[v], lane, v);
             }
-            Chooser<uint32_t, V, MODE == BY_LOGIT16> c(key, lane);
+            Choose c(key, lane);
             bool near = false;
-            if (groups) {
-                const float err = MODE == BY_SCORE ? p.group_top * (softmax ? 5.3e-6f / z : 5e-7f) : 0.f;
+            if (p.GK < p.G) {
+                const float err = MODE == BY_LOGIT ? 0.f : p.group_top * (MODE == BY_SOFTMAX ? 5.3e-6f * rz : 5e-7f);
                 float t1, t2;
                 if (p.lane_groups) {
-                    if (MODE == BY_SCORE && by_logit) {
-                        t1 = t2 = -INFINITY;
+                    t1 = t2 = -INFINITY;
 #pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            t2 = fmaxf(t2, fminf(t1, s[v]));
-                            t1 = fmaxf(t1, s[v]);
-                        }
-                    } else if (MODE == BY_LOGIT16) {  // one value per group counts here
-                        t1 = key_float((c.k1 & 0x80000000u) ? c.k1 & ~LOW13 : c.k1 | LOW13);
-                        t2 = -INFINITY;
-                    } else {
-                        t1 = key_float(c.k1);
-                        t2 = key_float(c.k2);
+                    for (int v = 0; v < V; ++v) {
+                        t2 = fmaxf(t2, fminf(t1, s[v]));
+                        t1 = fmaxf(t1, s[v]);
                     }
                     join_top2(t1, t2, p.lp_log2);
                     if (!group_open(p, t1, t2, lane, err, near)) {
 #pragma unroll
-                        for (int v = 0; v < V; ++v)
-                            key[v] = MODE == BY_LOGIT16 ? (KEY_CLOSED & ~LOW13) | (LOW13 - expert_of<V>(lane, v)) : KEY_CLOSED;
-                        c.k1 = key[0]; c.v1 = 0;
-                        c.k2 = key[1]; c.v2 = 1;
+                        for (int v = 0; v < V; ++v) key[v] = Choose::key_of(-INFINITY, lane, v);
+#pragma unroll
+                        for (int d = 0; d < Choose::D; ++d) c.k[d] = key[d];
                     }
                 } else {
                     group_top2<V>(p, s, s_row, lane, t1, t2);
@@ -470,10 +514,9 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel
                     for (int v = 0; v < V; ++v) {
                         const int e = expert_of<V>(lane, v);
                         const int g = e < p.E ? (e * p.gmul) >> 20 : 0;
-                        if (!((open >> (g << p.lp_log2)) & 1u))
-                            key[v] = MODE == BY_LOGIT16 ? (KEY_CLOSED & ~LOW13) | (LOW13 - e) : KEY_CLOSED;
+                        if (!((open >> (g << p.lp_log2)) & 1u)) key[v] = Choose::key_of(-INFINITY, lane, v);
                     }
-                    c.restart();
+                    c.list(~0u);
                 }
             }
 #pragma unroll 1
@@ -481,14 +524,17 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel
                 c.next();
                 if (lane == r * p.slots + j) { my_key = c.best; my_e = c.e; }
             }
-            if (MODE == BY_SCORE && !by_logit && p.k < p.E) {
+            if (!UNIQUE && p.k < p.E) {
                 // the border's other side: the first that is no tie, in 64 bits too, of the last one chosen
                 const uint32_t last = c.best;
                 const int le = c.e;
                 c.next();
                 for (int n = p.k + 1; c.best == last && last > KEY_CLOSED; ++n) {
                     const T *row = logits + (t0 + r) * p.ld;
-                    if (to_f32(row[c.e]) != to_f32(row[le]) || p.bias[c.e] != p.bias[le]) { near = true; break; }
+                    if (to_f32(row[c.e]) != to_f32(row[le]) || (p.bias != nullptr && p.bias[c.e] != p.bias[le])) {
+                        near = true;
+                        break;
+                    }
                     if (n >= p.E) { c.best = KEY_NONE; break; }
                     c.next();
                 }
@@ -504,39 +550,33 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel
         // ---- the rows together
         const bool mine = seg < rows && slot < p.k;
         const T *row = logits + (t0 + (seg < rows ? seg : 0)) * p.ld;
-        bool my_open;
-        float my_x = 0.f;
-        if (MODE == BY_LOGIT16) {
-            my_open = (my_key | LOW13) > KEY_CLOSED;
-            my_x = key_float((my_key & 0x80000000u) ? my_key & ~LOW13 : my_key | LOW13);
-        } else {
-            my_open = my_key > KEY_CLOSED;
-            my_x = MODE == BY_LOGIT32 ? key_float(my_key) : mine ? to_f32(row[my_e]) : 0.f;
-        }
-        if (MODE == BY_SCORE) {
-            if (!by_logit) {
-                // neighbours closer than their errors, unless they are the same logit
-                // and bias (a tie in 64 bits too, which the index has broken)
-                const float my_s = key_float(my_key), my_b = mine ? p.bias[my_e] : 0.f;
-                const float my_err = score_error(p.score, my_s, fabsf(my_s - my_b), my_z);
-                float s2 = __shfl_down_sync(FULL, my_s, 1), err2 = __shfl_down_sync(FULL, my_err, 1);
-                const float x2 = __shfl_down_sync(FULL, my_x, 1), b2 = __shfl_down_sync(FULL, my_b, 1);
-                bool open2 = __shfl_down_sync(FULL, static_cast<int>(my_open), 1) != 0;
-                bool tie = my_x == x2 && my_b == b2;
-                if (slot == p.k - 1) {
-                    s2 = key_float(border);
-                    open2 = border > KEY_CLOSED;
-                    tie = false;
-                    // the border's own error: its p is at most the chosen one's s less the least bias; bounded by p = 1
-                    err2 = score_error(p.score, s2, p.score == KOSMOS_SCORE_SIGMOID ? 0.f : 1.0f / my_z, my_z);
-                }
-                my_near = my_near || (my_open && open2 && !(my_s - s2 > my_err + err2) && !tie);
-                my_near = my_near && mine;
+        bool my_open = (my_key | MASK) > KEY_CLOSED;
+        float my_x;
+        if (UNIQUE) my_x = key_float((my_key & 0x80000000u) ? my_key & ~MASK : my_key | MASK);
+        else my_x = mine ? to_f32(row[my_e]) : 0.f;
+        if (!UNIQUE) {
+            // neighbours closer than their errors, unless they are the same logit
+            // and bias (a tie in 64 bits too, which the index has broken)
+            const float rz = MODE == BY_SOFTMAX ? rcp(my_z) : 1.f;
+            const float my_b = mine && p.bias != nullptr ? p.bias[my_e] : 0.f;
+            const float my_p = MODE == BY_LOGIT ? my_x : fast_p<MODE>(my_x, my_m, rz);
+            const float my_s = MODE == BY_LOGIT ? my_x : my_p + my_b;
+            const float my_err = score_error<MODE>(my_s, my_p, rz);
+            float s2 = __shfl_down_sync(FULL, my_s, 1), err2 = __shfl_down_sync(FULL, my_err, 1);
+            const float x2 = __shfl_down_sync(FULL, my_x, 1), b2 = __shfl_down_sync(FULL, my_b, 1);
+            bool open2 = __shfl_down_sync(FULL, static_cast<int>(my_open), 1) != 0;
+            bool tie = my_x == x2 && my_b == b2;
+            if (slot == p.k - 1) {  // everything that is left is at most the border's value; its p is at most 1 / z
+                s2 = key_float(border | MASK);
+                open2 = (border | MASK) > KEY_CLOSED;
+                err2 = score_error<MODE>(s2, rz, rz);
+                tie = false;
             }
-            const uint32_t nb = __ballot_sync(FULL, my_near && seg < rows);
+            my_near = mine && (my_near || (my_open && open2 && !(my_s - s2 > my_err + err2) && !tie));
+            const uint32_t nb = __ballot_sync(FULL, my_near);
             if (nb != 0u) {
                 for (int r = 0; r < rows; ++r) {
-                    if (((nb >> (r * p.slots)) & (p.slots == 32 ? FULL : (1u << p.slots) - 1u)) == 0u) continue;
+                    if (((nb >> (r * p.slots)) & ((1u << p.slots) - 1u)) == 0u) continue;
                     int ce = 0;
                     bool co = false;
                     choose_f64<T, V>(p, logits + (t0 + r) * p.ld, lane, ce, co);
@@ -620,8 +660,9 @@ template <typename T, int MODE> kosmos_status launch_route_m(const RouteParams &
 }
 
 template <typename T> kosmos_status launch_route_t(const RouteParams &p, int sms, cudaStream_t stream) {
-    if (p.bias != nullptr || (p.GK < p.G && p.group_top == 2)) return launch_route_m<T, BY_SCORE>(p, sms, stream);
-    return launch_route_m<T, sizeof(T) == 2 ? BY_LOGIT16 : BY_LOGIT32>(p, sms, stream);
+    if (p.bias == nullptr && !(p.GK < p.G && p.group_top == 2)) return launch_route_m<T, BY_LOGIT>(p, sms, stream);
+    if (p.score == KOSMOS_SCORE_SIGMOID) return launch_route_m<T, BY_SIGMOID>(p, sms, stream);
+    return launch_route_m<T, BY_SOFTMAX>(p, sms, stream);
 }
 
 struct RouteBwdParams {
