@@ -70,17 +70,17 @@ template <typename F> __device__ __forceinline__ F warp_sum(F v) {
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(FULL, v, d);
     return v;
 }
-// The gates of the chosen experts (p.slots lanes per row; logit x, open or
+// The gates of the chosen experts (slots lanes per row; logit x, open or
 // closed).  m, z: the row's maximum and sum of exponentials (softmax without
 // renorm).  Ratios of p are taken relative to the largest chosen one, so that
 // small scores keep their precision.
-__device__ __forceinline__ float route_gate(const RouteParams &p, float x, bool open, float m, float z) {
+__device__ __forceinline__ float route_gate(const RouteParams &p, int slots, float x, bool open, float m, float z) {
     if (!p.renorm) {
         if (!open) return 0.f;
         return p.scale * (p.score == KOSMOS_SCORE_SOFTMAX ? expf(x - m) / z : 1.0f / (1.0f + expf(-x)));
     }
     float top = open ? x : -INFINITY;
-    for (int d = p.slots / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
+    for (int d = slots / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
     float w = 0.f;
     if (open) {
         if (p.score == KOSMOS_SCORE_SOFTMAX) {
@@ -91,7 +91,7 @@ __device__ __forceinline__ float route_gate(const RouteParams &p, float x, bool 
         }
     }
     float sum = w;
-    for (int d = p.slots / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
+    for (int d = slots / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
     return open ? p.scale * (w / sum) : 0.f;
 }
 
@@ -105,7 +105,7 @@ enum RouteMode : int { BY_LOGIT = 0, BY_SIGMOID = 1, BY_SOFTMAX = 2 };
 // Order-preserving map of floats to unsigned integers (-0 as +0).  Closed
 // experts have the key of -inf, and so have the places beyond E, which
 // come last of all because ties go to the lower expert.
-constexpr uint32_t KEY_NONE = 0u, KEY_CLOSED = 0x007FFFFFu, LOW13 = 0x1FFFu;
+constexpr uint32_t KEY_NONE = 0u, KEY_CLOSED = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t float_key(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);
     return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
@@ -233,26 +233,25 @@ __device__ __forceinline__ void group_top2(const RouteParams &p, const float *s,
     join_top2(t1, t2, p.lp_log2);
 }
 
-// The row's experts in their order, one per call of next(): a warp-wide
-// maximum over the lanes' lists of their best D values; a lane that has given
-// its list away makes the next one.  A key's low bits tell a lane's values
-// apart.  UNIQUE (16-bit logits, whose order takes 19 bits): they hold the expert,
-// so the maximum tells which one it is.  Otherwise they hold V - 1 - v, the
-// order of values is that without the low bits, and of equal ones the
-// lowest lane, which holds the lower experts, comes first.
-template <int V, bool UNIQUE> struct Chooser {
-    static constexpr int D = V <= 4 ? V : V == 8 ? 4 : 2;
-    static constexpr uint32_t MASK = UNIQUE ? LOW13 : V - 1;
+// The row's experts in the order of their keys, one per call of next(): a
+// warp-wide maximum over the lanes' lists of their best D keys; a lane that has
+// given its list away makes the next one.  A key's low bits hold the expert
+// (as MASK - e: the lower expert first), so keys differ and the maximum tells
+// whose it is; a value's own low bits are lost, which matters to fp32 values
+// only (a bf16 or fp16 value has at least 13 zero bits).
+template <int V> struct Chooser {
+    static constexpr int D = V <= 4 ? V : 2;
+    static constexpr uint32_t MASK = 32 * V - 1;
     const uint32_t *key;
-    int lane;
     uint32_t k[D];
-    uint32_t best = KEY_NONE;  // value (low bits set unless UNIQUE) and expert of the last call
-    int e = 0;
+    uint32_t best = KEY_NONE;
 
     static __device__ __forceinline__ uint32_t key_of(float f, int lane, int v) {
-        return (float_key(f) & ~MASK) | (MASK - (UNIQUE ? expert_of<V>(lane, v) : v));
+        return (float_key(f) & ~MASK) | (MASK - expert_of<V>(lane, v));
     }
-    __device__ __forceinline__ Chooser(const uint32_t *keys, int l) : key(keys), lane(l) { list(~0u); }
+    static __device__ __forceinline__ int expert(uint32_t key) { return static_cast<int>(MASK - (key & MASK)); }
+    static __device__ __forceinline__ bool is_open(uint32_t key) { return (key | MASK) > KEY_CLOSED; }
+    __device__ __forceinline__ explicit Chooser(const uint32_t *keys) : key(keys) { list(~0u); }
     // the largest D keys below limit
     __device__ __forceinline__ void list(uint32_t limit) {
 #pragma unroll
@@ -269,25 +268,14 @@ template <int V, bool UNIQUE> struct Chooser {
         }
     }
     __device__ __forceinline__ void next() {
-        const uint32_t given = k[0];
-        bool won;
-        if (UNIQUE) {
-            best = __reduce_max_sync(FULL, k[0]);
-            e = static_cast<int>(MASK - (best & MASK));
-            won = k[0] == best;
-        } else {
-            best = __reduce_max_sync(FULL, k[0] | MASK);
-            const int src = __ffs(__ballot_sync(FULL, (k[0] | MASK) == best)) - 1;
-            e = expert_of<V>(src, static_cast<int>(MASK - (__shfl_sync(FULL, k[0], src) & MASK)));
-            won = lane == src;
-        }
-        if (won) {
+        best = __reduce_max_sync(FULL, k[0]);
+        if (k[0] == best) {
 #pragma unroll
             for (int d = 0; d + 1 < D; ++d) k[d] = k[d + 1];
             k[D - 1] = KEY_NONE;
         }
         if (D < V && __any_sync(FULL, k[0] == KEY_NONE)) {
-            if (k[0] == KEY_NONE) list(given);
+            if (k[0] == KEY_NONE) list(best);  // what is left of every lane is below best
         }
     }
 };
@@ -329,14 +317,21 @@ __device__ __forceinline__ double key_double(uint64_t k) {
     return __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
 }
 
-// Chooses the row's experts by their 64-bit selection scores; lane j < k gets
-// the j-th expert and whether it is open.  Comparisons are of integer keys:
-// fp64 instructions are rare here (two lanes a cycle) and a row in this
-// function is waited for.
+// One row whose experts are chosen by their 64-bit selection scores, from the
+// logits to the outputs.  Comparisons are of integer keys: fp64 instructions
+// are slow here (two lanes a cycle) and the row is waited for.
 template <typename T, int V>
-__device__ __noinline__ void choose_f64(const RouteParams &p, const T *row, int lane, int &my_e, bool &my_open) {
+__device__ __noinline__ void route_row_f64(const RouteParams &p, int64_t t, int lane, int32_t *s_hist) {
+    const T *row = static_cast<const T *>(p.logits) + t * p.ld;
     alignas(16) T raw[V];
     load_row<T, V>(row, p.E, lane, p.vec, raw);
+    bool nan = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float x = to_f32(raw[v]);
+        nan = nan || x != x || (x == INFINITY && p.score == KOSMOS_SCORE_SOFTMAX);
+    }
+    nan = __any_sync(FULL, nan);
     const bool by_logit = p.bias == nullptr;
     double m = 0.0, z = 1.0;
     if (p.score == KOSMOS_SCORE_SOFTMAX) {
@@ -399,21 +394,38 @@ __device__ __noinline__ void choose_f64(const RouteParams &p, const T *row, int 
         for (int v = 0; v < V; ++v)
             if (key[v] > KEY64_CLOSED) key[v] = double_key(static_cast<double>(to_f32(raw[v])));
     }
+    int my_e = 0;
+    bool my_open = false;
     for (int j = 0; j < p.k; ++j) {
         const Best64 b = take_best64<V>(key, lane);
         if (lane == j) { my_e = b.e; my_open = b.key > KEY64_CLOSED; }
     }
+    const bool mine = lane < p.k;
+    float g = route_gate(p, 16, mine ? to_f32(row[my_e]) : 0.f, mine && my_open, static_cast<float>(m), static_cast<float>(z));
+    if (nan) g = NAN;
+    if (mine) {
+        p.idx[t * p.k + lane] = my_e;
+        p.gate[t * p.k + lane] = g;
+        if (p.counts != nullptr) atomicAdd(&s_hist[my_e], 1);
+    }
 }
 
-// A warp takes p.rows consecutive rows at a time (slots lanes each, a power of
-// two): the rows are ordered one after the other, and their gates are then
-// computed together, lane r * slots + j holding row r's j-th choice.
+// A warp takes p.rows consecutive rows at a time, with p.slots lanes for each
+// (a power of two, at least k): the rows are ordered one after the other, and
+// the rest is done for them together, lane r * slots + j holding row r's j-th
+// candidate.  Candidates beyond the k-th are taken while their keys differ from
+// the k-th's in the expert alone; the candidates are then ranked by their
+// scores in full.  What the scores' errors leave open goes to a list (LATER rows
+// per warp) and is done at the end by route_row_f64: a call here would keep
+// the loop's values out of registers.
+constexpr int LATER = 16;
+
 template <typename T, int V, int MODE>
 __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel(const __grid_constant__ RouteParams p) {
-    constexpr bool UNIQUE = MODE == BY_LOGIT && sizeof(T) == 2;
-    using Choose = Chooser<V, UNIQUE>;
-    constexpr uint32_t MASK = Choose::MASK;
+    constexpr bool EXACT = MODE == BY_LOGIT && sizeof(T) == 2;  // keys hold their values whole
+    using Choose = Chooser<V>;
     extern __shared__ int32_t s_mem[];
+    __shared__ int64_t s_later[ROUTE_WARPS][LATER];
     int32_t *s_hist = s_mem;                                           // [E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *s_row = reinterpret_cast<float *>(s_mem + p.hist_words) + warp * p.row_words;
@@ -423,177 +435,185 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? MINB : 1) route_kernel
     }
     const bool softmax = MODE == BY_SOFTMAX || (MODE == BY_LOGIT && p.score == KOSMOS_SCORE_SOFTMAX);
     const bool need_z = MODE == BY_SOFTMAX || (softmax && !p.renorm);
-    float bias[V];
-    if (MODE != BY_LOGIT) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = expert_of<V>(lane, v);
-            bias[v] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.f;
-        }
-    }
     const T *logits = static_cast<const T *>(p.logits);
     const int seg = lane / p.slots, slot = lane % p.slots;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * ROUTE_WARPS * p.rows;
     int64_t t0 = (static_cast<int64_t>(blockIdx.x) * ROUTE_WARPS + warp) * p.rows;
-    alignas(16) T next[V];
-    if (t0 < p.T) load_row<T, V>(logits + t0 * p.ld, p.E, lane, p.vec, next);
-    for (; t0 < p.T; t0 += stride) {
-        uint32_t my_key = KEY_NONE, border = KEY_NONE;
-        int my_e = 0;
-        float my_m = 0.f, my_z = 1.f;
-        bool my_nan = false, my_near = false;
-        const int rows = p.T - t0 < p.rows ? static_cast<int>(p.T - t0) : p.rows;
-#pragma unroll 1
-        for (int r = 0; r < rows; ++r) {
-            float x[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) x[v] = to_f32(next[v]);
-            const int64_t tn = r + 1 < rows ? t0 + r + 1 : t0 + stride;
-            if (tn < p.T) load_row<T, V>(logits + tn * p.ld, p.E, lane, p.vec, next);
-            bool nan = false;
-            float m = -INFINITY, z = 1.f;
+    while (t0 < p.T) {
+        float bias[V];
+        if (MODE != BY_LOGIT) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                nan = nan || x[v] != x[v];
-                if (MODE != BY_SIGMOID) x[v] = fmaxf(x[v], -INFINITY);  // NaN: closed
+                const int e = expert_of<V>(lane, v);
+                bias[v] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.f;
             }
-            if (softmax) {
+        }
+        int later = 0;
+        alignas(16) T next[V];
+        load_row<T, V>(logits + t0 * p.ld, p.E, lane, p.vec, next);
+        for (; t0 < p.T && later <= LATER - p.rows; t0 += stride) {
+            uint32_t my_key = KEY_NONE, border = KEY_NONE;
+            float my_m = 0.f, my_z = 1.f;
+            bool my_nan = false, my_near = false;
+            int most = p.k;  // candidates of the longest row
+            const int rows = p.T - t0 < p.rows ? static_cast<int>(p.T - t0) : p.rows;
+#pragma unroll 1
+            for (int r = 0; r < rows; ++r) {
+                float x[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
-                nan = nan || m == INFINITY;
-            }
-            nan = __any_sync(FULL, nan);
-            // s: what orders the experts and scores the groups; closed experts -inf
-            float s[V];
-            if (need_z) {
-                m = key_float(__reduce_max_sync(FULL, float_key(m)));
-                if (m == -INFINITY) m = 0.f;
-                z = 0.f;
+                for (int v = 0; v < V; ++v) x[v] = to_f32(next[v]);
+                const int64_t tn = r + 1 < rows ? t0 + r + 1 : t0 + stride;
+                if (tn < p.T) load_row<T, V>(logits + tn * p.ld, p.E, lane, p.vec, next);
+                bool nan = false;
+                float m = -INFINITY, z = 1.f;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    s[v] = ex2(LOG2E * (x[v] - m));
-                    z += s[v];
+                    nan = nan || x[v] != x[v];
+                    if (MODE != BY_SIGMOID) x[v] = fmaxf(x[v], -INFINITY);  // NaN: closed
                 }
-                z = warp_sum(z);
-            }
-            const float rz = MODE == BY_SOFTMAX ? rcp(z) : 1.f;
-            uint32_t key[V];
+                if (softmax) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (MODE == BY_LOGIT) {
-                    s[v] = x[v];
-                } else {
-                    const float q = MODE == BY_SOFTMAX ? s[v] * rz : fast_p<BY_SIGMOID>(x[v], 0.f, 1.f);
-                    s[v] = x[v] > -INFINITY ? fmaxf(q + bias[v], -INFINITY) : -INFINITY;
+                    for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
+                    nan = nan || m == INFINITY;
                 }
-                key[v] = Choose::key_of(s[v], lane, v);
-            }
-            Choose c(key, lane);
-            bool near = false;
-            if (p.GK < p.G) {
-                const float err = MODE == BY_LOGIT ? 0.f : p.group_top * (MODE == BY_SOFTMAX ? 5.3e-6f * rz : 5e-7f);
-                float t1, t2;
-                if (p.lane_groups) {
-                    t1 = t2 = -INFINITY;
+                nan = __any_sync(FULL, nan);
+                // s: what orders the experts and scores the groups; closed experts -inf
+                float s[V];
+                if (need_z) {
+                    m = key_float(__reduce_max_sync(FULL, float_key(m)));
+                    if (m == -INFINITY) m = 0.f;
+                    z = 0.f;
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        t2 = fmaxf(t2, fminf(t1, s[v]));
-                        t1 = fmaxf(t1, s[v]);
+                        s[v] = ex2(LOG2E * (x[v] - m));
+                        z += s[v];
                     }
-                    join_top2(t1, t2, p.lp_log2);
-                    if (!group_open(p, t1, t2, lane, err, near)) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) key[v] = Choose::key_of(-INFINITY, lane, v);
-#pragma unroll
-                        for (int d = 0; d < Choose::D; ++d) c.k[d] = key[d];
-                    }
-                } else {
-                    group_top2<V>(p, s, s_row, lane, t1, t2);
-                    const uint32_t open = __ballot_sync(FULL, group_open(p, t1, t2, lane, err, near));
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int e = expert_of<V>(lane, v);
-                        const int g = e < p.E ? (e * p.gmul) >> 20 : 0;
-                        if (!((open >> (g << p.lp_log2)) & 1u)) key[v] = Choose::key_of(-INFINITY, lane, v);
-                    }
-                    c.list(~0u);
+                    z = warp_sum(z);
                 }
-            }
+                const float rz = MODE == BY_SOFTMAX ? rcp(z) : 1.f;
+                uint32_t key[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (MODE == BY_LOGIT) {
+                        s[v] = x[v];
+                    } else {
+                        const float q = MODE == BY_SOFTMAX ? s[v] * rz : fast_p<BY_SIGMOID>(x[v], 0.f, 1.f);
+                        s[v] = x[v] > -INFINITY ? fmaxf(q + bias[v], -INFINITY) : -INFINITY;
+                    }
+                    key[v] = Choose::key_of(s[v], lane, v);
+                }
+                bool near = false;
+                if (p.GK < p.G) {
+                    const float err = MODE == BY_LOGIT ? 0.f : p.group_top * (MODE == BY_SOFTMAX ? 5.3e-6f * rz : 5e-7f);
+                    float t1, t2;
+                    if (p.lane_groups) {
+                        t1 = t2 = -INFINITY;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            t2 = fmaxf(t2, fminf(t1, s[v]));
+                            t1 = fmaxf(t1, s[v]);
+                        }
+                        join_top2(t1, t2, p.lp_log2);
+                        if (!group_open(p, t1, t2, lane, err, near)) {
+#pragma unroll
+                            for (int v = 0; v < V; ++v) key[v] = Choose::key_of(-INFINITY, lane, v);
+                        }
+                    } else {
+                        group_top2<V>(p, s, s_row, lane, t1, t2);
+                        const uint32_t open = __ballot_sync(FULL, group_open(p, t1, t2, lane, err, near));
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            const int e = expert_of<V>(lane, v);
+                            const int g = e < p.E ? (e * p.gmul) >> 20 : 0;
+                            if (!((open >> (g << p.lp_log2)) & 1u)) key[v] = Choose::key_of(-INFINITY, lane, v);
+                        }
+                    }
+                }
+                Choose c(key);
+                const int first = r * p.slots;
 #pragma unroll 1
-            for (int j = 0; j < p.k; ++j) {
-                c.next();
-                if (lane == r * p.slots + j) { my_key = c.best; my_e = c.e; }
-            }
-            if (!UNIQUE && p.k < p.E) {
-                // the border's other side: the first that is no tie, in 64 bits too, of the last one chosen
-                const uint32_t last = c.best;
-                const int le = c.e;
-                c.next();
-                for (int n = p.k + 1; c.best == last && last > KEY_CLOSED; ++n) {
-                    const T *row = logits + (t0 + r) * p.ld;
-                    if (to_f32(row[c.e]) != to_f32(row[le]) || (p.bias != nullptr && p.bias[c.e] != p.bias[le])) {
-                        near = true;
-                        break;
-                    }
-                    if (n >= p.E) { c.best = KEY_NONE; break; }
+                for (int j = 0; j < p.k; ++j) {
                     c.next();
+                    if (lane == first + j) my_key = c.best;
+                }
+                if (!EXACT && p.k < p.E) {
+                    const uint32_t last = c.best | Choose::MASK;
+                    c.next();
+                    int n = p.k;
+                    for (; (c.best | Choose::MASK) == last && last > KEY_CLOSED && n < p.slots && n + 1 < p.E; ++n) {
+                        if (lane == first + n) my_key = c.best;
+                        c.next();
+                    }
+                    near = near || ((c.best | Choose::MASK) == last && last > KEY_CLOSED);
+                    if (n > most) most = n;
+                }
+                if (seg == r) {
+                    border = p.k < p.E ? c.best : KEY_NONE;
+                    my_nan = nan;
+                    my_near = near;
+                    my_m = m;
+                    my_z = z;
                 }
             }
-            if (seg == r) {
-                border = c.best;
-                my_nan = nan;
-                my_near = near;
-                my_m = m;
-                my_z = z;
-            }
-        }
-        // ---- the rows together
-        const bool mine = seg < rows && slot < p.k;
-        const T *row = logits + (t0 + (seg < rows ? seg : 0)) * p.ld;
-        bool my_open = (my_key | MASK) > KEY_CLOSED;
-        float my_x;
-        if (UNIQUE) my_x = key_float((my_key & 0x80000000u) ? my_key & ~MASK : my_key | MASK);
-        else my_x = mine ? to_f32(row[my_e]) : 0.f;
-        if (!UNIQUE) {
-            // neighbours closer than their errors, unless they are the same logit
-            // and bias (a tie in 64 bits too, which the index has broken)
-            const float rz = MODE == BY_SOFTMAX ? rcp(my_z) : 1.f;
-            const float my_b = mine && p.bias != nullptr ? p.bias[my_e] : 0.f;
-            const float my_p = MODE == BY_LOGIT ? my_x : fast_p<MODE>(my_x, my_m, rz);
-            const float my_s = MODE == BY_LOGIT ? my_x : my_p + my_b;
-            const float my_err = score_error<MODE>(my_s, my_p, rz);
-            float s2 = __shfl_down_sync(FULL, my_s, 1), err2 = __shfl_down_sync(FULL, my_err, 1);
-            const float x2 = __shfl_down_sync(FULL, my_x, 1), b2 = __shfl_down_sync(FULL, my_b, 1);
-            bool open2 = __shfl_down_sync(FULL, static_cast<int>(my_open), 1) != 0;
-            bool tie = my_x == x2 && my_b == b2;
-            if (slot == p.k - 1) {  // everything that is left is at most the border's value; its p is at most 1 / z
-                s2 = key_float(border | MASK);
-                open2 = (border | MASK) > KEY_CLOSED;
-                err2 = score_error<MODE>(s2, rz, rz);
-                tie = false;
-            }
-            my_near = mine && (my_near || (my_open && open2 && !(my_s - s2 > my_err + err2) && !tie));
-            const uint32_t nb = __ballot_sync(FULL, my_near);
-            if (nb != 0u) {
-                for (int r = 0; r < rows; ++r) {
+            // ---- the rows together
+            const bool mine = my_key != KEY_NONE;
+            const T *row = logits + (t0 + (seg < rows ? seg : 0)) * p.ld;
+            const bool my_open = mine && Choose::is_open(my_key);
+            const int my_e = mine ? Choose::expert(my_key) : 0;
+            const float my_x = EXACT ? key_float((my_key & 0x80000000u) ? my_key & ~Choose::MASK : my_key | Choose::MASK)
+                                     : to_f32(row[my_e]);
+            int rank = mine ? slot : p.k;
+            if (!EXACT) {
+                // ranked by the score in full; equal scores keep the keys' order,
+                // which is that of the experts
+                const float rz = MODE == BY_SOFTMAX ? rcp(my_z) : 1.f;
+                const float my_b = MODE != BY_LOGIT && p.bias != nullptr ? p.bias[my_e] : 0.f;
+                const float my_p = fast_p<MODE>(my_x, my_m, rz);
+                const float my_s = !my_open ? -INFINITY : MODE == BY_LOGIT ? my_x : my_p + my_b;
+                const float my_err = score_error<MODE>(my_s, my_p, rz);
+                bool close = false;
+                rank = mine ? 0 : p.k;
+                for (int o = 0; o < most; ++o) {
+                    const float so = __shfl_sync(FULL, my_s, seg * p.slots + o);
+                    rank += (so > my_s || (so == my_s && o < slot)) ? 1 : 0;
+                    // a pair within its errors: the wider one's is at least half of their sum
+                    if (MODE != BY_LOGIT) close = close || (o != slot && fabsf(so - my_s) <= 2.f * my_err);
+                }
+                if (MODE != BY_LOGIT && __any_sync(FULL, close && mine)) {
+                    // unless they are the same logit and bias: a tie in 64 bits too
+                    for (int o = 0; o < most; ++o) {
+                        const int src = seg * p.slots + o;
+                        const float so = __shfl_sync(FULL, my_s, src), eo = __shfl_sync(FULL, my_err, src);
+                        const float xo = __shfl_sync(FULL, my_x, src), bo = __shfl_sync(FULL, my_b, src);
+                        const bool oo = __shfl_sync(FULL, static_cast<int>(my_open), src) != 0;
+                        if (my_open && oo && !(fabsf(so - my_s) > my_err + eo) && !(xo == my_x && bo == my_b)) my_near = true;
+                    }
+                }
+                if (mine && rank == p.k - 1 && my_open && Choose::is_open(border)) {
+                    // everything that is left is at most the border's value, its p at most 1 / z
+                    const float sb = key_float(border | Choose::MASK);
+                    if (!(my_s - sb > my_err + score_error<MODE>(sb, rz, rz))) my_near = true;
+                }
+                uint32_t nb = __ballot_sync(FULL, my_near && mine);
+                for (int r = 0; nb != 0u && r < rows; ++r) {
                     if (((nb >> (r * p.slots)) & ((1u << p.slots) - 1u)) == 0u) continue;
-                    int ce = 0;
-                    bool co = false;
-                    choose_f64<T, V>(p, logits + (t0 + r) * p.ld, lane, ce, co);
-                    ce = __shfl_sync(FULL, ce, slot);
-                    const int coi = __shfl_sync(FULL, static_cast<int>(co), slot);
-                    if (seg == r) { my_e = ce; my_open = coi != 0; }
+                    if (lane == 0) s_later[warp][later] = t0 + r;
+                    ++later;
+                    if (seg == r) rank = p.k;  // not now
                 }
-                if (mine) my_x = to_f32(row[my_e]);
+            }
+            float g = route_gate(p, p.slots, my_x, my_open && rank < p.k, my_m, my_z);
+            if (my_nan) g = NAN;
+            if (rank < p.k) {
+                const int64_t at = (t0 + seg) * p.k + rank;
+                p.idx[at] = my_e;
+                p.gate[at] = g;
+                if (p.counts != nullptr) atomicAdd(&s_hist[my_e], 1);
             }
         }
-        float g = route_gate(p, my_x, mine && my_open, my_m, my_z);
-        if (my_nan) g = NAN;
-        if (mine) {
-            p.idx[(t0 + seg) * p.k + slot] = my_e;
-            p.gate[(t0 + seg) * p.k + slot] = g;
-            if (p.counts != nullptr) atomicAdd(&s_hist[my_e], 1);
-        }
+        __syncwarp();
+        for (int i = 0; i < later; ++i) route_row_f64<T, V>(p, s_later[warp][i], lane, s_hist);
+        __syncwarp();
     }
     if (p.counts == nullptr) return;
     __syncthreads();
@@ -627,7 +647,7 @@ template <typename T, int MODE> kosmos_status launch_route_m(const RouteParams &
     p.vec = p.E % w == 0 && reinterpret_cast<uintptr_t>(p.logits) % (w * es) == 0 && p.ld * es % (w * es) == 0;
     // several rows per warp share the gates' arithmetic, once every warp has
     // some; before that a row's latency counts
-    p.slots = p.k <= 8 ? 8 : 16;
+    p.slots = MODE == BY_LOGIT && es == 2 && p.k <= 8 ? 8 : 16;
     p.rows = p.T >= ROUTE_ROWS_FROM * static_cast<int64_t>(sms) ? 32 / p.slots : 1;
     int64_t blocks = cdiv(p.T, ROUTE_WARPS * p.rows);
     if (blocks > MINB * static_cast<int64_t>(sms)) blocks = MINB * static_cast<int64_t>(sms);
