@@ -216,6 +216,22 @@ def test_scores_next_to_one_another(K, score):
         check_route(K, x.cuda(), {"topk": k, "score": score, **kw}, bias.cuda())
 
 
+@pytest.mark.parametrize("bits", [23, 30, 37, 43, 49])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_next_to_one_another(K, score, bits):
+    """A few distinct logits and biases that are multiples of 2^-bits: order,
+    borders and groups are decided by differences of that size.  The
+    multiples add to the scores exactly in 64 bits, so that groups whose sums
+    agree are ties there too."""
+    T, E = 40, 96
+    g = torch.Generator().manual_seed(9)
+    x = torch.randint(0, 3, (T, E), generator=g).float() * 0.5
+    bias = torch.randint(-20, 21, (E,), generator=g).float() * 2.0 ** -bits
+    for k, kw in ((7, {}), (8, {"n_groups": 8, "topk_groups": 3, "group_top": 2}),
+                  (12, {"n_groups": 12, "topk_groups": 5, "group_top": 1})):
+        check_route(K, x.cuda(), {"topk": k, "score": score, **kw}, bias.cuda())
+
+
 def test_nan_and_infinite_logits(K):
     for score in ("softmax", "sigmoid"):
         for dtype in (torch.float32, torch.bfloat16):
