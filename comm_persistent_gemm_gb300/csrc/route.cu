@@ -18,53 +18,187 @@ struct RouteBwdParams {
     int64_t T, ld, ldd;
     int E, k, score, renorm;
     float scale;
+    // set by the launcher
+    bool vec_in;        // pieces of a logits row are loaded whole
+    int rows, slots;    // rows of a warp, lanes that hold a row's choices (chosen-only kernel)
+    int tile;           // bytes of a warp's rows in shared memory (a multiple of 16)
 };
 
-// One warp per token.
+// A warp's finished rows from shared memory to dlogits.  Rows that follow one
+// another there are one run of bytes, in 16-byte pieces where it starts on
+// such a boundary.
 template <typename T>
-__global__ void __launch_bounds__(BWD_THREADS) route_bwd_kernel(const __grid_constant__ RouteBwdParams p) {
-    extern __shared__ float s_rows[];
+__device__ __forceinline__ void store_rows(const RouteBwdParams &p, const T *tile, int64_t t0, int rows, int lane) {
+    T *out = static_cast<T *>(p.dlogits) + t0 * p.ldd;
+    const bool dense = p.ldd == p.E;
+    const int runs = dense ? 1 : rows, n = dense ? rows * p.E : p.E;
+    for (int r = 0; r < runs; ++r) {
+        T *o = out + r * p.ldd;
+        const T *s = tile + r * p.E;
+        int done = 0;
+        if ((reinterpret_cast<uintptr_t>(o) & 15u) == 0 && (r * p.E * sizeof(T)) % 16 == 0) {
+            const int n16 = static_cast<int>(n * sizeof(T) / 16);
+#pragma unroll 4
+            for (int i = lane; i < n16; i += 32)
+                reinterpret_cast<uint4 *>(o)[i] = reinterpret_cast<const uint4 *>(s)[i];
+            done = n16 * 16 / static_cast<int>(sizeof(T));
+        }
+        for (int i = done + lane; i < n; i += 32) o[i] = s[i];
+    }
+}
+
+// g dg of a choice (0 for a closed pick, whatever dg holds), and g dg less its
+// share of D / scale where the gates were renormalised.
+__device__ __forceinline__ float chosen_gradient(const RouteBwdParams &p, float g, float dg, float D) {
+    if (g == 0.f) return 0.f;
+    return p.renorm ? g * (dg - D / p.scale) : g * dg;
+}
+
+// Every score but the softmax without renorm: only the chosen experts have a
+// gradient.  A warp takes p.rows rows, lane r * slots + j their j-th choice, and
+// keeps them in shared memory, zero but for those.  Bound by the writes of
+// dlogits (and for the sigmoid a 32-byte sector read per choice).
+template <typename T>
+__global__ void __launch_bounds__(BWD_THREADS) route_bwd_chosen_kernel(const __grid_constant__ RouteBwdParams p) {
+    extern __shared__ uint4 s_mem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *srow = s_rows + warp * p.E;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * BWD_WARPS + warp; t < p.T;
-         t += static_cast<int64_t>(gridDim.x) * BWD_WARPS) {
-        const T *row = static_cast<const T *>(p.logits) + t * p.ld;
-        T *out = static_cast<T *>(p.dlogits) + t * p.ldd;
-        const int e = lane < p.k ? p.idx[t * p.k + lane] : -1;
+    T *tile = reinterpret_cast<T *>(reinterpret_cast<uint8_t *>(s_mem) + warp * p.tile);
+    for (int i = lane; i < p.tile / 16; i += 32) reinterpret_cast<uint4 *>(tile)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    const int r = lane / p.slots, j = lane % p.slots;
+    const T *logits = static_cast<const T *>(p.logits);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) * p.rows;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * p.rows; t0 < p.T; t0 += stride) {
+        const int rows = p.T - t0 < p.rows ? static_cast<int>(p.T - t0) : p.rows;
+        int e = -1;
+        float g = 0.f, dg = 0.f;
+        if (r < rows && j < p.k) {
+            const int64_t at = (t0 + r) * p.k + j;
+            e = p.idx[at];
+            g = p.gate[at];
+            dg = p.dgate[at];
+        }
         const bool ok = e >= 0 && e < p.E;
-        const float g = ok ? p.gate[t * p.k + lane] : 0.f;
-        const float dg = ok ? p.dgate[t * p.k + lane] : 0.f;
-        float gdg = g * dg;
-        if (g == 0.f) gdg = 0.f;  // a closed pick: no gradient, whatever dg holds
-        const float D = row_sum<32>(gdg);
-        float d = gdg;
-        if (p.renorm && g != 0.f) d = g * (dg - D / p.scale);
-        if (p.score == KOSMOS_SCORE_SIGMOID && ok && g != 0.f) d *= 1.0f / (1.0f + expf(to_f32(row[e])));
-        const bool full = p.score == KOSMOS_SCORE_SOFTMAX && !p.renorm;
-        for (int i = lane; i < p.E; i += 32) srow[i] = 0.f;
+        if (!ok) g = 0.f;
+        float x = 0.f;
+        if (p.score == KOSMOS_SCORE_SIGMOID && ok) x = to_f32(logits[(t0 + r) * p.ld + e]);
+        float D = g == 0.f ? 0.f : g * dg;
+        for (int d = p.slots / 2; d > 0; d >>= 1) D += __shfl_xor_sync(FULL, D, d);
+        float v = chosen_gradient(p, g, dg, D);
+        if (p.score == KOSMOS_SCORE_SIGMOID && g != 0.f) v *= 1.0f / (1.0f + expf(x));  // 1 - p
+        if (ok) tile[r * p.E + e] = from_f32<T>(v);
         __syncwarp();
-        if (ok) srow[e] = d;
+        store_rows(p, tile, t0, rows, lane);
         __syncwarp();
-        float m = -INFINITY, z = 0.f;
-        if (full) {
-            for (int i = lane; i < p.E; i += 32) m = fmaxf(m, to_f32(row[i]));
-            m = row_max<32>(m);
-            for (int i = lane; i < p.E; i += 32) z += expf(to_f32(row[i]) - m);
-            z = row_sum<32>(z);
-        }
-        for (int i = lane; i < p.E; i += 32) {
-            float v = srow[i];
-            if (full && D != 0.f) v -= D * (expf(to_f32(row[i]) - m) / z);  // D = 0 also where every pick is closed
-            out[i] = from_f32<T>(v);
-        }
+        if (ok) tile[r * p.E + e] = from_f32<T>(0.f);
         __syncwarp();
     }
 }
 
-template <typename T> kosmos_status launch_route_bwd_t(const RouteBwdParams &p, int sms, cudaStream_t stream) {
-    int64_t blocks = cdiv(p.T, BWD_WARPS);
-    if (blocks > 4ll * sms) blocks = 4ll * sms;
-    route_bwd_kernel<T><<<static_cast<unsigned>(blocks), BWD_THREADS, sizeof(float) * BWD_WARPS * p.E, stream>>>(p);
+// The softmax without renorm: every expert of a row has the gradient -p D, the
+// chosen ones g dg besides.  L lanes share a row, as in the forward.
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(BWD_THREADS) route_bwd_all_kernel(const __grid_constant__ RouteBwdParams p) {
+    using Lay = Layout<T, L, V>;
+    constexpr int R = 32 / L, N = L < KOSMOS_ROUTE_MAX_TOPK ? KOSMOS_ROUTE_MAX_TOPK / L : 1;
+    extern __shared__ uint4 s_mem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = lane / L, l = lane % L;
+    T *tile = reinterpret_cast<T *>(reinterpret_cast<uint8_t *>(s_mem) + warp * p.tile);
+    const T *logits = static_cast<const T *>(p.logits);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) * R;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * R; t0 < p.T; t0 += stride) {
+        const int rows = p.T - t0 < R ? static_cast<int>(p.T - t0) : R;
+        const bool live = seg < rows;
+        const int64_t t = live ? t0 + seg : t0;
+        const T *row = logits + t * p.ld;
+        float x[V];
+        Lay::load(row, p.E, l, p.vec_in, x);
+        int e[N];
+        float gdg[N], xe[N], D = 0.f;
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+            const int j = h * L + l;
+            e[h] = -1;
+            gdg[h] = xe[h] = 0.f;
+            if (live && j < p.k) {
+                const int64_t at = t * p.k + j;
+                e[h] = p.idx[at];
+                if (e[h] < 0 || e[h] >= p.E) e[h] = -1;
+                const float g = p.gate[at];
+                if (e[h] >= 0) {
+                    xe[h] = to_f32(row[e[h]]);
+                    if (g != 0.f) gdg[h] = g * p.dgate[at];
+                }
+            }
+            D += gdg[h];
+        }
+        D = row_sum<L>(D);
+        float m = x[0], z = 0.f;
+#pragma unroll
+        for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
+        m = row_max<L>(m);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = ex2(LOG2E * (x[v] - m));
+            z += x[v];
+        }
+        z = row_sum<L>(z);
+        // D is 0 where every pick is closed, a row of -inf with them
+        const float f = D != 0.f ? -D * rcp(z) : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int ev = Lay::expert(l, v);
+            if (live && ev < p.E) tile[seg * p.E + ev] = from_f32<T>(f != 0.f ? x[v] * f : 0.f);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < N; ++h)
+            if (e[h] >= 0) {
+                const float d = f != 0.f ? fmaf(ex2(LOG2E * (xe[h] - m)), f, gdg[h]) : gdg[h];
+                tile[seg * p.E + e[h]] = from_f32<T>(d);
+            }
+        __syncwarp();
+        store_rows(p, tile, t0, rows, lane);
+        __syncwarp();
+    }
+}
+
+template <typename T, int L, int V> kosmos_status launch_bwd_all(RouteBwdParams p, int sms, cudaStream_t stream) {
+    constexpr int R = 32 / L, run = Layout<T, L, V>::W * sizeof(T);
+    p.vec_in = p.E % Layout<T, L, V>::W == 0 && reinterpret_cast<uintptr_t>(p.logits) % run == 0 &&
+               p.ld * static_cast<int64_t>(sizeof(T)) % run == 0;
+    p.tile = static_cast<int>(align_up(R * p.E * sizeof(T), 16));
+    int warps = BWD_WARPS;
+    while (warps > 1 && cdiv(p.T, R * warps) < sms) warps /= 2;
+    int64_t blocks = cdiv(p.T, R * warps);
+    const int64_t most = 4ll * (BWD_WARPS / warps) * sms;
+    if (blocks > most) blocks = most;
+    route_bwd_all_kernel<T, L, V><<<static_cast<unsigned>(blocks), warps * 32, warps * p.tile, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? KOSMOS_OK : KOSMOS_ERR_CUDA;
+}
+
+template <typename T> kosmos_status launch_route_bwd_t(RouteBwdParams p, int sms, cudaStream_t stream) {
+    if (p.score == KOSMOS_SCORE_SOFTMAX && !p.renorm) {
+        if (p.E <= 32) return launch_bwd_all<T, 8, 4>(p, sms, stream);
+        if (p.E <= 64) return launch_bwd_all<T, 8, 8>(p, sms, stream);
+        if (p.E <= 128) return launch_bwd_all<T, 8, 16>(p, sms, stream);
+        if (p.E <= 256) return launch_bwd_all<T, 8, 32>(p, sms, stream);
+        if (p.E <= 512) return launch_bwd_all<T, 16, 32>(p, sms, stream);
+        return launch_bwd_all<T, 32, 32>(p, sms, stream);
+    }
+    // as many rows as a warp has lanes for their choices, within 4 KB of shared
+    // memory a warp; fewer where there are more warps than tokens for them
+    p.slots = 1;
+    while (p.slots < p.k) p.slots *= 2;
+    p.rows = 32 / p.slots;
+    while (p.rows > 1 && (p.rows * p.E * sizeof(T) > 4096 || cdiv(p.T, p.rows) < 2ll * sms)) p.rows /= 2;
+    p.tile = static_cast<int>(align_up(p.rows * p.E * sizeof(T), 16));
+    int warps = BWD_WARPS;
+    while (warps > 1 && cdiv(p.T, p.rows * warps) < sms) warps /= 2;
+    int64_t blocks = cdiv(p.T, p.rows * warps);
+    const int64_t most = 6ll * (BWD_WARPS / warps) * sms;
+    if (blocks > most) blocks = most;
+    route_bwd_chosen_kernel<T><<<static_cast<unsigned>(blocks), warps * 32, warps * p.tile, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? KOSMOS_OK : KOSMOS_ERR_CUDA;
 }
 
@@ -89,7 +223,7 @@ kosmos_status launch_route(const RouteLaunch &L, cudaStream_t stream) {
 }
 
 kosmos_status launch_route_bwd(const RouteBwdLaunch &L, cudaStream_t stream) {
-    RouteBwdParams p;
+    RouteBwdParams p = {};
     p.logits = L.logits; p.idx = L.idx; p.gate = L.gate; p.dgate = L.dgate; p.dlogits = L.dlogits;
     p.T = L.T; p.ld = L.ld; p.ldd = L.ldd; p.E = L.E; p.k = L.r.topk; p.score = L.r.score; p.renorm = L.r.renorm;
     p.scale = L.r.scale;

@@ -53,6 +53,47 @@ template <int L, typename F> __device__ __forceinline__ F row_sum(F v) {
     return v;
 }
 
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Which of a row's values a lane holds: pieces of W consecutive experts (one
+// load of up to 16 bytes), the row's lanes side by side.
+template <typename T, int L, int V> struct Layout {
+    static constexpr int W = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
+    static __device__ __forceinline__ int expert(int l, int v) { return (v / W) * L * W + l * W + v % W; }
+    // the values as floats; beyond E: -inf
+    static __device__ __forceinline__ void load(const T *row, int E, int l, bool vec, float *x) {
+#pragma unroll
+        for (int c = 0; c < V; c += W) {
+            const int e0 = expert(l, c);
+            alignas(16) T r[W];
+            if (vec) {
+                if (e0 < E) {
+                    if constexpr (W * sizeof(T) == 16)
+                        *reinterpret_cast<uint4 *>(r) = *reinterpret_cast<const uint4 *>(row + e0);
+                    else
+                        *reinterpret_cast<uint2 *>(r) = *reinterpret_cast<const uint2 *>(row + e0);
+                    static_assert(W * sizeof(T) >= 8, "a piece is 8 or 16 bytes");
+                }
+#pragma unroll
+                for (int i = 0; i < W; ++i) x[c + i] = e0 < E ? to_f32(r[i]) : -INFINITY;
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i) x[c + i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
+            }
+        }
+    }
+};
+
 // The forward launch for one type of logits (route_bf16.cu, route_fp16.cu, route_fp32.cu).
 kosmos_status launch_route_bf16(const RouteParams &p, int sms, cudaStream_t stream);
 kosmos_status launch_route_fp16(const RouteParams &p, int sms, cudaStream_t stream);

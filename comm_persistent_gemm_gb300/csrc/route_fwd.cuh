@@ -81,18 +81,6 @@ __device__ __forceinline__ float key_float(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-constexpr float LOG2E = 1.4426950408889634f;
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // p in fp32 (rz = 1 / z): x = -inf gives 0.
 __device__ __forceinline__ float fast_sigmoid(float x) { return rcp(1.0f + ex2(-LOG2E * x)); }
 __device__ __forceinline__ float fast_softmax(float x, float m, float rz) { return ex2(LOG2E * (x - m)) * rz; }
@@ -115,35 +103,6 @@ __device__ __forceinline__ dd score_dd(bool softmax, float x, float b, float m, 
     return dd_add(dd_mul(dd_exp(two_sum(x, -m)), rz), b);
 }
 __device__ __forceinline__ float difference(dd a, dd b) { return (a.hi - b.hi) + (a.lo - b.lo); }
-
-// Which of a row's values a lane holds: pieces of W consecutive experts (one
-// load of up to 16 bytes), the row's lanes side by side.
-template <typename T, int L, int V> struct Layout {
-    static constexpr int W = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
-    static __device__ __forceinline__ int expert(int l, int v) { return (v / W) * L * W + l * W + v % W; }
-    // the values as floats; beyond E: -inf
-    static __device__ __forceinline__ void load(const T *row, int E, int l, bool vec, float *x) {
-#pragma unroll
-        for (int c = 0; c < V; c += W) {
-            const int e0 = expert(l, c);
-            alignas(16) T r[W];
-            if (vec) {
-                if (e0 < E) {
-                    if constexpr (W * sizeof(T) == 16)
-                        *reinterpret_cast<uint4 *>(r) = __ldg(reinterpret_cast<const uint4 *>(row + e0));
-                    else
-                        *reinterpret_cast<uint2 *>(r) = __ldg(reinterpret_cast<const uint2 *>(row + e0));
-                    static_assert(W * sizeof(T) >= 8, "a piece is 8 or 16 bytes");
-                }
-#pragma unroll
-                for (int i = 0; i < W; ++i) x[c + i] = e0 < E ? to_f32(r[i]) : -INFINITY;
-            } else {
-#pragma unroll
-                for (int i = 0; i < W; ++i) x[c + i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
-            }
-        }
-    }
-};
 
 // A lane's best D keys in order.  A key's low bits hold the expert (as
 // MASK - e: the lower expert first), so keys differ and a maximum tells
