@@ -165,8 +165,8 @@ def opts(**kw) -> Opts:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
+        import torch
         # the current device's current stream without building a Stream
         # object for it (0.3 instead of 3 us a call)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -387,23 +387,32 @@ def router(topk: int, score: int = SCORE_SOFTMAX, n_groups: int = 1, topk_groups
 
 
 _plain_dtypes = {}
+_int32 = _float32 = None
+
+
+def _load_types():
+    """The router and gradient operators' types, once torch is needed."""
+    global _int32, _float32
+    import torch
+    _int32, _float32 = torch.int32, torch.float32
+    _plain_dtypes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
 
 
 def _plain_dtype(t) -> int:
-    if not _plain_dtypes:
-        import torch
-        _plain_dtypes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
     d = _plain_dtypes.get(t.dtype)
     if d is None:
         raise ValueError(f"kosmos: bf16, fp16 or fp32 expected, not {t.dtype}")
     return d
 
 
-def _check_like(what: str, t, dtype, shape):
-    """t: a contiguous CUDA tensor of this type and shape."""
-    if not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} and shape {shape} expected, got "
-                         f"{t.dtype} {tuple(t.shape)}")
+def _like(t, dtype, shape) -> bool:
+    """t is a contiguous CUDA tensor of this type and shape."""
+    return t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _unlike(what: str, t, dtype, shape):
+    raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} and shape {shape} expected, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
 
 
 def _rows(what: str, t):
@@ -436,42 +445,55 @@ def route(logits, r: Router, topk_idx, topk_gate, bias=None, expert_counts=None,
     stride.  bias [experts] fp32 takes part in the choice only.
     expert_counts [experts] int32 receives the tokens per expert and needs
     ws = route_workspace(experts)."""
-    import torch
+    if _int32 is None:
+        _load_types()
     T, E, ld = _rows("route: logits", logits)
     shape = (T, r.topk)
-    _check_like("route: topk_idx", topk_idx, torch.int32, shape)
-    _check_like("route: topk_gate", topk_gate, torch.float32, shape)
+    if not _like(topk_idx, _int32, shape):
+        _unlike("route: topk_idx", topk_idx, _int32, shape)
+    if not _like(topk_gate, _float32, shape):
+        _unlike("route: topk_gate", topk_gate, _float32, shape)
     b = c = w = None
     nbytes = 0
     if bias is not None:
-        _check_like("route: bias", bias, torch.float32, (E,))
+        if not _like(bias, _float32, (E,)):
+            _unlike("route: bias", bias, _float32, (E,))
         b = bias.data_ptr()
     if expert_counts is not None:
-        _check_like("route: expert_counts", expert_counts, torch.int32, (E,))
+        if not _like(expert_counts, _int32, (E,)):
+            _unlike("route: expert_counts", expert_counts, _int32, (E,))
         c = expert_counts.data_ptr()
     if ws is not None:
-        _check_cuda(ws)
-        w, nbytes = ws.data_ptr(), ws.numel()
-    rc = lib().kosmos_route(logits.data_ptr(), _plain_dtype(logits), T, E, ld, r, b, topk_idx.data_ptr(),
-                            topk_gate.data_ptr(), c, w, nbytes, _stream(stream))
-    _raise(rc, "kosmos_route")
+        if not (ws.is_cuda and ws.is_contiguous()):
+            _check_cuda(ws)
+        w, nbytes = ws.data_ptr(), ws.nbytes
+    rc = (_lib or lib()).kosmos_route(logits.data_ptr(), _plain_dtype(logits), T, E, ld, r, b, topk_idx.data_ptr(),
+                                      topk_gate.data_ptr(), c, w, nbytes, _stream(stream))
+    if rc != OK:
+        _raise(rc, "kosmos_route")
 
 
 def route_bwd(logits, r: Router, topk_idx, topk_gate, dgate, dlogits, stream=None):
     """dlogits (the logits' type) from dgate: the gradient of route's gates
     with the choice of experts held fixed."""
-    import torch
+    if _int32 is None:
+        _load_types()
     T, E, ld = _rows("route_bwd: logits", logits)
     T2, E2, ldd = _rows("route_bwd: dlogits", dlogits)
     if dlogits.dtype is not logits.dtype or T2 != T or E2 != E:
         raise ValueError("route_bwd: dlogits needs the logits' type and shape")
     shape = (T, r.topk)
-    _check_like("route_bwd: topk_idx", topk_idx, torch.int32, shape)
-    _check_like("route_bwd: topk_gate", topk_gate, torch.float32, shape)
-    _check_like("route_bwd: dgate", dgate, torch.float32, shape)
-    rc = lib().kosmos_route_bwd(logits.data_ptr(), _plain_dtype(logits), T, E, ld, r, topk_idx.data_ptr(),
-                                topk_gate.data_ptr(), dgate.data_ptr(), dlogits.data_ptr(), ldd, _stream(stream))
-    _raise(rc, "kosmos_route_bwd")
+    if not _like(topk_idx, _int32, shape):
+        _unlike("route_bwd: topk_idx", topk_idx, _int32, shape)
+    if not _like(topk_gate, _float32, shape):
+        _unlike("route_bwd: topk_gate", topk_gate, _float32, shape)
+    if not _like(dgate, _float32, shape):
+        _unlike("route_bwd: dgate", dgate, _float32, shape)
+    rc = (_lib or lib()).kosmos_route_bwd(logits.data_ptr(), _plain_dtype(logits), T, E, ld, r, topk_idx.data_ptr(),
+                                          topk_gate.data_ptr(), dgate.data_ptr(), dlogits.data_ptr(), ldd,
+                                          _stream(stream))
+    if rc != OK:
+        _raise(rc, "kosmos_route_bwd")
 
 
 class GradSet:
@@ -481,6 +503,8 @@ class GradSet:
     given).  It keeps the tensors alive and reads them anew in every call."""
 
     def __init__(self, grads: Sequence, outs: Optional[Sequence] = None):
+        if _int32 is None:
+            _load_types()
         self.grads = list(grads)
         self.outs = list(outs) if outs is not None else self.grads
         if len(self.outs) != len(self.grads):
@@ -514,29 +538,34 @@ def grad_norm(grads, norm, ws, tensor_norms=None, stream=None):
     """norm (fp32, one element) = the 2-norm of all gradients together (a
     GradSet or a list of tensors); tensor_norms (fp32, one per tensor) = the
     norm of each."""
-    import torch
     s = _grad_set(grads)
-    _check_like("grad_norm: norm", norm, torch.float32, (1,))
+    if not _like(norm, _float32, (1,)):
+        _unlike("grad_norm: norm", norm, _float32, (1,))
     each = None
     if tensor_norms is not None:
-        _check_like("grad_norm: tensor_norms", tensor_norms, torch.float32, (s.n,))
+        if not _like(tensor_norms, _float32, (s.n,)):
+            _unlike("grad_norm: tensor_norms", tensor_norms, _float32, (s.n,))
         each = tensor_norms.data_ptr()
-    _check_cuda(ws)
-    rc = lib().kosmos_grad_norm(s.ptrs, s.sizes, s.dtypes, s.n, norm.data_ptr(), each, ws.data_ptr(), ws.numel(),
-                                _stream(stream))
-    _raise(rc, "kosmos_grad_norm")
+    if not (ws.is_cuda and ws.is_contiguous()):
+        _check_cuda(ws)
+    rc = (_lib or lib()).kosmos_grad_norm(s.ptrs, s.sizes, s.dtypes, s.n, norm.data_ptr(), each, ws.data_ptr(),
+                                          ws.nbytes, _stream(stream))
+    if rc != OK:
+        _raise(rc, "kosmos_grad_norm")
 
 
 def grad_clip(grads, max_norm: float, norm, ws, stream=None):
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or
     into the GradSet's outs; norm (fp32, one element) receives the norm."""
-    import torch
     s = _grad_set(grads)
-    _check_like("grad_clip: norm", norm, torch.float32, (1,))
-    _check_cuda(ws)
-    rc = lib().kosmos_grad_clip(s.ptrs, s.out_ptrs, s.sizes, s.dtypes, s.n, max_norm, norm.data_ptr(), ws.data_ptr(),
-                                ws.numel(), _stream(stream))
-    _raise(rc, "kosmos_grad_clip")
+    if not _like(norm, _float32, (1,)):
+        _unlike("grad_clip: norm", norm, _float32, (1,))
+    if not (ws.is_cuda and ws.is_contiguous()):
+        _check_cuda(ws)
+    rc = (_lib or lib()).kosmos_grad_clip(s.ptrs, s.out_ptrs, s.sizes, s.dtypes, s.n, max_norm, norm.data_ptr(),
+                                          ws.data_ptr(), ws.nbytes, _stream(stream))
+    if rc != OK:
+        _raise(rc, "kosmos_grad_clip")
 
 
 def mxfp8_scale_bytes(rows: int, cols: int, along_cols: bool) -> int:

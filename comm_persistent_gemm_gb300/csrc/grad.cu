@@ -9,7 +9,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "common.cuh"
+#include <cstring>
+
+#include "engine.cuh"
 #include "launch.h"
 
 namespace kosmos {
@@ -288,17 +290,14 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const __grid_co
         v = block_sum(v, s_red);
         if (threadIdx.x == 0) p.part[c] = v;
     }
-    if (threadIdx.x == 0) {
-        __threadfence();
-        s_last = atomicAdd(&p.hdr->done_ctas, 1u) == gridDim.x - 1;
-    }
+    // thread 0 wrote the block's sums and releases them with its arrival
+    if (threadIdx.x == 0) s_last = atom_add_acqrel_gpu(&p.hdr->done_ctas, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!s_last) return;
     // The last block joins the chunks, tensor by tensor, in their order: a
     // thread takes a tensor of few chunks (a set of many small tensors then
     // waits for memory once, not once per tensor), a warp one of many.
     constexpr int FEW = 8;
-    __threadfence();
     for (int j = threadIdx.x; j < p.nt; j += GRAD_THREADS) {
         const int b = p.chunk0[j], e = p.chunk0[j + 1];
         if (e - b > FEW) continue;
@@ -354,6 +353,135 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_scale_kernel(const __grid_c
     }
 }
 
+// A small set in one launch: every block holds one chunk in registers (its
+// 16-byte pieces, four per thread, and an element at its ends), the blocks meet
+// once their sums are written, each adds all of them up and scales what
+// it holds.  Against the two launches this saves the second one's start and
+// its reads.  The launch is cooperative, so every block is resident; the wait is
+// bounded all the same and reports KOSMOS_ERR_TIMEOUT.
+constexpr int HELD = static_cast<int>(GRAD_MIN_CHUNK / 16 / GRAD_THREADS);
+constexpr uint64_t MEET_LIMIT_NS = 2000000000ull;
+
+template <typename T> __device__ __forceinline__ double held_squares(const uint4 *w, float rest) {
+    using Wd = Words<T>;
+    float s = 0.f;
+    uint32_t any = 0u;
+    auto each = [&](auto &&f) {
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) {
+            const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[Wd::EPW];
+                Wd::unpack(ww[i], v);
+#pragma unroll
+                for (int e = 0; e < Wd::EPW; ++e) f(v[e], ww[i]);
+            }
+        }
+    };
+    each([&](float v, uint32_t raw) { s = fmaf(v, v, s); any |= raw & Wd::MAGNITUDE; });
+    const double r = rest;
+    if (!out_of_range(s, any)) return static_cast<double>(s) + r * r;
+    double acc = r * r;
+    each([&](float v, uint32_t) { acc += static_cast<double>(v) * v; });
+    return acc;
+}
+
+template <typename T>
+__device__ __forceinline__ void held_store(const uint4 *w, float rest, T *out, bool vec, int64_t head, int nv, int64_t n,
+                                           float coef) {
+    using Wd = Words<T>;
+    constexpr int VE = 4 * Wd::EPW;
+#pragma unroll
+    for (int u = 0; u < HELD; ++u) {
+        const int j = threadIdx.x + u * GRAD_THREADS;
+        if (j >= nv) break;
+        uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v[Wd::EPW];
+            Wd::unpack(ww[i], v);
+#pragma unroll
+            for (int e = 0; e < Wd::EPW; ++e) {
+                v[e] *= coef;
+                if (!vec) Wd::store(out + head + static_cast<int64_t>(j) * VE + i * Wd::EPW + e, v[e]);
+            }
+            ww[i] = Wd::pack(v);
+        }
+        if (vec) reinterpret_cast<uint4 *>(out + head)[j] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
+    }
+    if (threadIdx.x < n - static_cast<int64_t>(nv) * VE) {
+        const int64_t i = threadIdx.x < head ? threadIdx.x : threadIdx.x + static_cast<int64_t>(nv) * VE;
+        Wd::store(out + i, rest * coef);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void clip_held(const T *x, T *out, int64_t n, WsHeader *hdr, double *part, int chunks,
+                                          float max_norm, float *norm_out, double *s_red, float *s_coef) {
+    constexpr int VE = 4 * Words<T>::EPW;
+    const int64_t head = head_elems(x, n);
+    const int nv = static_cast<int>((n - head) / VE);
+    uint4 w[HELD];
+#pragma unroll
+    for (int u = 0; u < HELD; ++u) {
+        const int j = threadIdx.x + u * GRAD_THREADS;
+        w[u] = j < nv ? ld_last(reinterpret_cast<const uint4 *>(x + head) + j) : make_uint4(0, 0, 0, 0);
+    }
+    float rest = 0.f;
+    if (threadIdx.x < n - static_cast<int64_t>(nv) * VE)
+        rest = Words<T>::load(x + (threadIdx.x < head ? threadIdx.x : threadIdx.x + static_cast<int64_t>(nv) * VE));
+    double v = block_sum(held_squares<T>(w, rest), s_red);
+    if (threadIdx.x == 0) {
+        if (blockIdx.x < chunks) part[blockIdx.x] = v;
+        (void)atom_add_acqrel_gpu(&hdr->tickets[0], 1u);
+        *s_coef = wait_flag_eq(hdr, &hdr->tickets[0], gridDim.x, MEET_LIMIT_NS, blockIdx.x) ? 1.f : -1.f;
+    }
+    __syncthreads();
+    if (*s_coef < 0.f) return;
+    v = 0.0;
+    for (int c = threadIdx.x; c < chunks; c += GRAD_THREADS) v += __ldcg(&part[c]);
+    v = block_sum(v, s_red);
+    if (threadIdx.x == 0) {
+        const float norm = sqrt_f32(v);
+        *s_coef = clip_factor(max_norm, norm, v);
+        if (blockIdx.x == 0) norm_out[0] = norm;
+        // the last to have read the sums makes the words ready for the next call
+        if (atom_add_acqrel_gpu(&hdr->tickets[1], 1u) == gridDim.x - 1) hdr->tickets[0] = hdr->tickets[1] = 0u;
+    }
+    __syncthreads();
+    const float coef = *s_coef;
+    if (coef == 1.0f && out == x) return;
+    held_store<T>(w, rest, out, ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0, head, nv, n,
+                  coef);
+}
+
+template <int N>
+__global__ void __launch_bounds__(GRAD_THREADS, 4) grad_clip_kernel(const __grid_constant__ GradParams<N> p) {
+    __shared__ double s_red[GRAD_THREADS / 32];
+    __shared__ float s_coef;
+    int64_t e0 = 0, e1 = 0;
+    int i = 0, dtype = KOSMOS_FP32;
+    const uint8_t *x = nullptr;
+    uint8_t *out = nullptr;
+    if (p.chunks > 0) {
+        i = tensor_of(p, blockIdx.x);
+        chunk_range(p, i, blockIdx.x, e0, e1);
+        dtype = p.dtype[i];
+        x = static_cast<const uint8_t *>(p.t[i].x);
+        out = static_cast<uint8_t *>(p.t[i].out);
+    }
+    if (dtype == KOSMOS_BF16)
+        clip_held(reinterpret_cast<const __nv_bfloat16 *>(x) + e0, reinterpret_cast<__nv_bfloat16 *>(out) + e0, e1 - e0, p.hdr,
+                  p.part, p.chunks, p.max_norm, p.norm, s_red, &s_coef);
+    else if (dtype == KOSMOS_FP16)
+        clip_held(reinterpret_cast<const __half *>(x) + e0, reinterpret_cast<__half *>(out) + e0, e1 - e0, p.hdr, p.part,
+                  p.chunks, p.max_norm, p.norm, s_red, &s_coef);
+    else
+        clip_held(reinterpret_cast<const float *>(x) + e0, reinterpret_cast<float *>(out) + e0, e1 - e0, p.hdr, p.part, p.chunks,
+                  p.max_norm, p.norm, s_red, &s_coef);
+}
+
 int elem_bytes(int dtype) { return dtype == KOSMOS_FP32 ? 4 : 2; }
 
 // Chunks are large enough that a large set has about GRAD_CHUNKS of them
@@ -399,6 +527,22 @@ template <int N> kosmos_status launch_grad_n(const GradLaunch &L, int64_t chunk_
             // and 559 us with eight (norm of 4.8 GB: 660 us, 709 us with two)
             int64_t blocks = chunks < 4ll * L.sms ? chunks : 4ll * L.sms;
             if (blocks < 1) blocks = 1;
+            if (L.outs != nullptr && p.first && p.last && chunk_bytes == GRAD_MIN_CHUNK && chunks <= 4ll * L.sms) {
+                // clipping a set of at most one chunk for each of four blocks per SM
+                cudaLaunchConfig_t cfg;
+                memset(&cfg, 0, sizeof(cfg));
+                cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+                cfg.blockDim = dim3(GRAD_THREADS);
+                cfg.stream = stream;
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeCooperative;
+                attr[0].val.cooperative = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                if (cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, p) == cudaSuccess) return KOSMOS_OK;
+                (void)cudaGetLastError();
+                return KOSMOS_ERR_CUDA;
+            }
             if (pass == 0)
                 grad_norm_kernel<N><<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, stream>>>(p);
             else if (chunks > 0)

@@ -135,12 +135,6 @@ __device__ __forceinline__ void red_relaxed_add_gpu(uint32_t *p, uint32_t v) {
     asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ uint32_t atom_add_acqrel_gpu(uint32_t *p, uint32_t v) {
-    uint32_t old;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-    return old;
-}
-
 // Publish one item into a ready queue: reserve an index, write the item, then
 // release its per-item flag (epoch-tagged).
 __device__ __forceinline__ void queue_put(uint32_t *tail, int32_t *items, uint32_t *flags, int cap, int32_t code,

@@ -104,6 +104,32 @@ def test_clip_into_outputs(K, shift, out_shift, max_norm):
     check_clip(K, grads, max_norm, outs)
 
 
+BIG = [0, 2500001, 31, 4000003, 1, 1800000, 700001]  # 23 MB: more than one launch holds
+
+
+@pytest.mark.parametrize("shift,out_shift", [(0, 0), (1, 1), (1, 0), (3, 5)])
+def test_clip_of_a_larger_set(K, shift, out_shift):
+    grads = ragged(51, shift, BIG)
+    outs = [torch.empty(g.numel() + 8, dtype=g.dtype, device="cuda")[(i * out_shift) % 8:][:g.numel()]
+            for i, g in enumerate(grads)]
+    check_clip(K, grads, 1.0, outs)
+    check_clip(K, grads, 1.0)
+    check_norm(K, grads)
+
+
+def test_norm_and_clip_agree_and_share_a_workspace(K):
+    """One workspace through calls of every kind, in turn."""
+    for sizes in (SIZES, BIG):
+        grads = ragged(61, 1, sizes)
+        s = K.GradSet(grads, [torch.empty_like(g) for g in grads])
+        ws, a, b = K.grad_workspace(s), torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+        for _ in range(3):
+            K.grad_norm(s, a, ws)
+            K.grad_clip(s, 1.0, b, ws)
+            assert abs(float(a) - float(b)) <= 2 * U * float(a)
+        assert K.status_sync(ws) == (K.OK, -1)
+
+
 def test_clip_in_place_and_guards(K):
     bufs = [torch.full((n + 16,), 3.0, dtype=DTS[i % 3], device="cuda") for i, n in enumerate(SIZES)]
     grads = [b[8:8 + n] for b, n in zip(bufs, SIZES)]
