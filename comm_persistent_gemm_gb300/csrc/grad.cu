@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const __grid_co
     __shared__ double s_red[GRAD_THREADS / 32];
     __shared__ double s_sum[N];
     __shared__ int s_last;
+    pdl_wait();
     // Blocks take every gridDim-th chunk, so that the whole grid reads one
     // stretch of memory at a time.
     for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const __grid_co
         v = block_sum(v, s_red);
         if (threadIdx.x == 0) p.part[c] = v;
     }
+    pdl_trigger();
     // thread 0 wrote the block's sums and releases them with its arrival
     if (threadIdx.x == 0) s_last = atom_add_acqrel_gpu(&p.hdr->done_ctas, 1u) == gridDim.x - 1;
     __syncthreads();
@@ -336,6 +338,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const __grid_co
 
 template <int N>
 __global__ void __launch_bounds__(GRAD_THREADS) grad_scale_kernel(const __grid_constant__ GradParams<N> p) {
+    pdl_wait();
     const float coef = p.scr->coef;
     // from the back, where the norm's pass ended: what it read last is still in L2
     for (int c = p.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
@@ -543,11 +546,11 @@ template <int N> kosmos_status launch_grad_n(const GradLaunch &L, int64_t chunk_
                 (void)cudaGetLastError();
                 return KOSMOS_ERR_CUDA;
             }
-            if (pass == 0)
-                grad_norm_kernel<N><<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, stream>>>(p);
-            else if (chunks > 0)
-                grad_scale_kernel<N><<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, stream>>>(p);
-            if (cudaGetLastError() != cudaSuccess) return KOSMOS_ERR_CUDA;
+            if (pass == 0 || chunks > 0) {
+                const kosmos_status st = launch_overlapped(pass == 0 ? &grad_norm_kernel<N> : &grad_scale_kernel<N>,
+                                                           static_cast<unsigned>(blocks), GRAD_THREADS, 0, stream, p);
+                if (st != KOSMOS_OK) return st;
+            }
             i0 += nt;
         } while (i0 < L.n);
     }

@@ -152,6 +152,27 @@ kosmos_status launch_mxfp8_quantize(const void *x, int64_t rows, int64_t cols, i
 kosmos_status launch_rail_decode(int op, int P, int64_t m, int64_t n, int order, int rank, int rail, int tile_m,
                                  int64_t split,
                                  int32_t *out, int64_t count, cudaStream_t stream);
+// Launch of a kernel that calls pdl_wait() (ptx.cuh) before it touches global
+// memory: its start overlaps the end of the stream's previous kernel, about
+// 1.5 us between short kernels.
+template <typename P>
+kosmos_status launch_overlapped(void (*kernel)(P), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                                const P &params) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, params) == cudaSuccess) return KOSMOS_OK;
+    (void)cudaGetLastError();
+    return KOSMOS_ERR_CUDA;
+}
+
 // Routing and gradient operators (route.cu, grad.cu): arguments are validated
 // by the C ABI; these pick the kernel variant and launch.
 struct RouteLaunch {

@@ -158,6 +158,13 @@ __device__ __forceinline__ uint32_t ld_relaxed_gpu(const uint32_t *p) {
     asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
+// Programmatic dependent launch.  A kernel launched by launch_overlapped may
+// start while the stream's previous kernel finishes; it must call pdl_wait()
+// before it touches global memory (the previous kernels are complete and their
+// writes visible then).  pdl_trigger() lets the next such kernel start early.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 __device__ __forceinline__ uint32_t atom_add_acqrel_gpu(uint32_t *p, uint32_t v) {
     uint32_t old;
     asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");

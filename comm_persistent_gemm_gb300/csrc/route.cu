@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(BWD_THREADS) route_bwd_chosen_kernel(const __g
     T *tile = reinterpret_cast<T *>(reinterpret_cast<uint8_t *>(s_mem) + warp * p.tile);
     for (int i = lane; i < p.tile / 16; i += 32) reinterpret_cast<uint4 *>(tile)[i] = make_uint4(0, 0, 0, 0);
     __syncwarp();
+    pdl_wait();
     const int r = lane / p.slots, j = lane % p.slots;
     const T *logits = static_cast<const T *>(p.logits);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) * p.rows;
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(BWD_THREADS) route_bwd_all_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = lane / L, l = lane % L;
     T *tile = reinterpret_cast<T *>(reinterpret_cast<uint8_t *>(s_mem) + warp * p.tile);
     const T *logits = static_cast<const T *>(p.logits);
+    pdl_wait();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) * R;
     for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * R; t0 < p.T; t0 += stride) {
         const int rows = p.T - t0 < R ? static_cast<int>(p.T - t0) : R;
@@ -173,8 +175,8 @@ template <typename T, int L, int V> kosmos_status launch_bwd_all(RouteBwdParams 
     int64_t blocks = cdiv(p.T, R * warps);
     const int64_t most = 4ll * (BWD_WARPS / warps) * sms;
     if (blocks > most) blocks = most;
-    route_bwd_all_kernel<T, L, V><<<static_cast<unsigned>(blocks), warps * 32, warps * p.tile, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KOSMOS_OK : KOSMOS_ERR_CUDA;
+    return launch_overlapped(&route_bwd_all_kernel<T, L, V>, static_cast<unsigned>(blocks), warps * 32, warps * p.tile, stream,
+                             p);
 }
 
 template <typename T> kosmos_status launch_route_bwd_t(RouteBwdParams p, int sms, cudaStream_t stream) {
@@ -198,8 +200,7 @@ template <typename T> kosmos_status launch_route_bwd_t(RouteBwdParams p, int sms
     int64_t blocks = cdiv(p.T, p.rows * warps);
     const int64_t most = 6ll * (BWD_WARPS / warps) * sms;
     if (blocks > most) blocks = most;
-    route_bwd_chosen_kernel<T><<<static_cast<unsigned>(blocks), warps * 32, warps * p.tile, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KOSMOS_OK : KOSMOS_ERR_CUDA;
+    return launch_overlapped(&route_bwd_chosen_kernel<T>, static_cast<unsigned>(blocks), warps * 32, warps * p.tile, stream, p);
 }
 
 }  // namespace

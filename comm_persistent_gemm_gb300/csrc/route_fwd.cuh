@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, MINB) route_kernel(const __grid
     if (p.GK < p.G)
         for (int i = l; i < p.row_words; i += L) s_row[i] = -INFINITY;
     __syncthreads();
+    pdl_wait();
     const bool softmax = MODE == BY_SOFTMAX || (MODE == BY_LOGIT && p.score == KOSMOS_SCORE_SOFTMAX);
     const bool need_z = MODE == BY_SOFTMAX || (softmax && !p.renorm);
     const T *logits = static_cast<const T *>(p.logits);
@@ -713,6 +714,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, MINB) route_kernel(const __grid
         for (int i = 0; i < later; ++i) route_row_f64<T, (L * V) / 32>(p, s_later[warp][i], lane, s_hist);
         __syncwarp();
     }
+    pdl_trigger();
     if (p.counts == nullptr) return;
     __syncthreads();
     if (gridDim.x == 1) {
@@ -761,8 +763,7 @@ kosmos_status launch_route_v(const RouteParams &q, int sms, cudaStream_t stream)
     int64_t blocks = cdiv(p.T, R * warps);
     const int64_t most = static_cast<int64_t>(MINB) * (ROUTE_WARPS / warps) * sms;
     if (blocks > most) blocks = most;
-    route_kernel<T, L, V, MODE><<<static_cast<unsigned>(blocks), warps * 32, smem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KOSMOS_OK : KOSMOS_ERR_CUDA;
+    return launch_overlapped(&route_kernel<T, L, V, MODE>, static_cast<unsigned>(blocks), warps * 32, smem, stream, p);
 }
 
 template <typename T, int MODE> kosmos_status launch_route_m(const RouteParams &p, int sms, cudaStream_t stream) {
