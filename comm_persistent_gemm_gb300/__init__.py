@@ -41,7 +41,8 @@ EXPORTS = ["kosmos_default_opts", "kosmos_num_sms", "kosmos_workspace_bytes", "k
            "kosmos_moe_workspace_bytes", "kosmos_moe_debug_view", "kosmos_ag_tile_plan", "kosmos_moe_bwd",
            "kosmos_moe_bwd_workspace_bytes", "kosmos_moe_bwd_debug_view", "kosmos_ag_gemm_host",
            "kosmos_noalloc_status_sync", "kosmos_default_router", "kosmos_route", "kosmos_route_workspace_bytes",
-           "kosmos_route_bwd", "kosmos_grad_norm", "kosmos_grad_clip", "kosmos_grad_workspace_bytes"]
+           "kosmos_route_bwd", "kosmos_grad_norm", "kosmos_grad_clip", "kosmos_grad_workspace_bytes",
+           "kosmos_moe_fwd_routed"]
 
 
 class KosmosError(RuntimeError):
@@ -134,6 +135,9 @@ def lib():
     L.kosmos_moe_bwd_debug_view.argtypes = [i32, i32, i64, i64, i32, i32, i64, vp, C.POINTER(vp), C.POINTER(i64)]
     L.kosmos_moe_bwd_debug_view.restype = i32
     L.kosmos_ag_tile_plan.restype = i32
+    L.kosmos_moe_fwd_routed.argtypes = [vp, i32, i64, i64, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                        C.c_size_t, C.POINTER(Opts), vp]
+    L.kosmos_moe_fwd_routed.restype = i32
     L.kosmos_default_router.argtypes = [C.POINTER(Router)]
     L.kosmos_default_router.restype = None
     L.kosmos_route.argtypes = [vp, i32, i64, i32, i64, C.POINTER(Router), vp, vp, vp, vp, vp, C.c_size_t, vp]
@@ -306,6 +310,33 @@ def moe_fwd(x_shards: List, w_router, w_gate: List, w_up: List, w_down: List, y_
                               topk_gate.data_ptr(), expert_counts.data_ptr(), dispatch_pos.data_ptr(),
                               ws.data_ptr(), ws.numel(), C.byref(o) if o is not None else None, _stream(stream))
     _raise(rc, "kosmos_moe_fwd")
+
+
+def moe_fwd_routed(x_shards: List, w_gate: List, w_up: List, w_down: List, y_shards: List, topk_idx, topk_gate,
+                   expert_counts, dispatch_pos, ws, o: Optional[Opts] = None, stream=None):
+    """moe_fwd (bf16) on a given routing: topk_idx and topk_gate are inputs
+    (from route), expert_counts and dispatch_pos outputs.  ws is
+    moe_workspace's; moe_bwd runs on it with a w_router of zeros."""
+    _check_cuda(*x_shards, *w_gate, *w_up, *w_down, *y_shards, topk_idx, topk_gate, expert_counts, dispatch_pos, ws)
+    if _int32 is None:
+        _load_types()
+    P = len(x_shards)
+    tokens = x_shards[0].shape[0] * P
+    hidden = x_shards[0].shape[1]
+    E = w_gate[0].shape[0] * P
+    inter = w_gate[0].shape[2]
+    topk = topk_idx.shape[1]
+    for what, t, dtype, shape in (("topk_idx", topk_idx, _int32, (tokens, topk)),
+                                  ("topk_gate", topk_gate, _float32, (tokens, topk)),
+                                  ("expert_counts", expert_counts, _int32, (E,)),
+                                  ("dispatch_pos", dispatch_pos, _int32, (tokens, topk))):
+        if not _like(t, dtype, shape):
+            _unlike(f"moe_fwd_routed: {what}", t, dtype, shape)
+    rc = lib().kosmos_moe_fwd_routed(_ptrs(x_shards), P, tokens, hidden, E, topk, inter, _ptrs(w_gate), _ptrs(w_up),
+                                     _ptrs(w_down), topk_idx.data_ptr(), topk_gate.data_ptr(), _ptrs(y_shards),
+                                     expert_counts.data_ptr(), dispatch_pos.data_ptr(), ws.data_ptr(), ws.numel(),
+                                     C.byref(o) if o is not None else None, _stream(stream))
+    _raise(rc, "kosmos_moe_fwd_routed")
 
 
 def moe_workspace(P: int, tokens: int, hidden: int, n_experts: int, topk: int, inter: int,

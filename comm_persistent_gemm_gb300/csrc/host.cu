@@ -625,8 +625,8 @@ kosmos_status kosmos_moe_debug_view(int what, int P, int64_t tokens, int64_t hid
                : KOSMOS_ERR_INVALID_ARG;
 }
 
-kosmos_status kosmos_moe_fwd(const void *const *x_shards, const void *w_router, int P, int64_t tokens, int64_t hidden,
-                             int n_experts, int topk, int64_t inter, const void *const *w_gate,
+static kosmos_status moe_fwd_call(bool routed, const void *const *x_shards, const void *w_router, int P, int64_t tokens,
+                             int64_t hidden, int n_experts, int topk, int64_t inter, const void *const *w_gate,
                              const void *const *w_gate_scales, const void *const *w_up,
                              const void *const *w_up_scales, const void *const *w_down,
                              const void *const *w_down_scales, int dtype, void *const *y_shards, int32_t *topk_idx,
@@ -646,7 +646,7 @@ kosmos_status kosmos_moe_fwd(const void *const *x_shards, const void *w_router, 
         if (mx && (!aligned16(w_gate_scales[q]) || !aligned16(w_up_scales[q]) || !aligned16(w_down_scales[q])))
             return KOSMOS_ERR_INVALID_ARG;
     }
-    if (!aligned16(w_router) || !aligned16(topk_idx) || !aligned16(topk_gate) || !aligned16(expert_counts) ||
+    if ((!routed && !aligned16(w_router)) || !aligned16(topk_idx) || !aligned16(topk_gate) || !aligned16(expert_counts) ||
         !aligned16(dispatch_pos))
         return KOSMOS_ERR_INVALID_ARG;
     if (!aligned16(ws)) return KOSMOS_ERR_WORKSPACE;
@@ -656,6 +656,7 @@ kosmos_status kosmos_moe_fwd(const void *const *x_shards, const void *w_router, 
     if (o.sched == KOSMOS_SCHED_FIXED || (o.sched == KOSMOS_SCHED_UNFUSED && o.trace)) return KOSMOS_ERR_UNSUPPORTED;
     if (o.link_gbs != 0) return KOSMOS_ERR_UNSUPPORTED;
     if (mx && (o.inject & KOSMOS_INJECT_IDENTITY_EXPERTS)) return KOSMOS_ERR_UNSUPPORTED;
+    if (routed && (o.sched != KOSMOS_SCHED_SELF || o.inject != 0)) return KOSMOS_ERR_UNSUPPORTED;
     if (ws_bytes < kosmos_moe_workspace_bytes(P, tokens, hidden, n_experts, topk, inter, dtype, &o))
         return KOSMOS_ERR_WORKSPACE;
     const int grid = grid_for(o);
@@ -675,11 +676,35 @@ kosmos_status kosmos_moe_fwd(const void *const *x_shards, const void *w_router, 
         L.y[q] = y_shards[q];
     }
     L.dtype = dtype;
+    L.routed = routed;
     L.wr = w_router;
     L.topk_idx = topk_idx; L.topk_gate = topk_gate; L.counts = expert_counts; L.pos = dispatch_pos;
     L.ws = ws; L.sched = o.sched; L.n_comm = 0; L.trace = o.trace; L.grid = grid; L.plain_launch = o.plain_launch;
     L.wait_limit_ns = o.wait_limit_ns; L.inject = o.inject;
     return launch_moe_fwd(L, static_cast<cudaStream_t>(stream));
+}
+
+kosmos_status kosmos_moe_fwd(const void *const *x_shards, const void *w_router, int P, int64_t tokens, int64_t hidden,
+                             int n_experts, int topk, int64_t inter, const void *const *w_gate,
+                             const void *const *w_gate_scales, const void *const *w_up,
+                             const void *const *w_up_scales, const void *const *w_down,
+                             const void *const *w_down_scales, int dtype, void *const *y_shards, int32_t *topk_idx,
+                             float *topk_gate, int32_t *expert_counts, int32_t *dispatch_pos, void *ws,
+                             size_t ws_bytes, const kosmos_opts *opts, void *stream) {
+    return moe_fwd_call(false, x_shards, w_router, P, tokens, hidden, n_experts, topk, inter, w_gate, w_gate_scales, w_up,
+                        w_up_scales, w_down, w_down_scales, dtype, y_shards, topk_idx, topk_gate, expert_counts,
+                        dispatch_pos, ws, ws_bytes, opts, stream);
+}
+
+kosmos_status kosmos_moe_fwd_routed(const void *const *x_shards, int P, int64_t tokens, int64_t hidden, int n_experts,
+                                    int topk, int64_t inter, const void *const *w_gate, const void *const *w_up,
+                                    const void *const *w_down, const int32_t *topk_idx, const float *topk_gate,
+                                    void *const *y_shards, int32_t *expert_counts, int32_t *dispatch_pos, void *ws,
+                                    size_t ws_bytes, const kosmos_opts *opts, void *stream) {
+    // the launch does not write a given routing
+    return moe_fwd_call(true, x_shards, nullptr, P, tokens, hidden, n_experts, topk, inter, w_gate, nullptr, w_up, nullptr,
+                        w_down, nullptr, KOSMOS_BF16, y_shards, const_cast<int32_t *>(topk_idx),
+                        const_cast<float *>(topk_gate), expert_counts, dispatch_pos, ws, ws_bytes, opts, stream);
 }
 
 static bool moe_bwd_sizes_ok(int P, int64_t tokens, int64_t hidden, int n_experts, int topk, int64_t inter) {

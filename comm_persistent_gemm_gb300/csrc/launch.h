@@ -70,6 +70,7 @@ struct MoeLaunch {
     const void *wus[KOSMOS_MAX_P];
     const void *wds[KOSMOS_MAX_P];
     int dtype;
+    bool routed;                    // topk_idx and topk_gate are given: no router
     void *y[KOSMOS_MAX_P];
     int32_t *topk_idx;
     float *topk_gate;

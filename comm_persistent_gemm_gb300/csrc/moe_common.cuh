@@ -194,6 +194,84 @@ __device__ __forceinline__ int warp_excl_scan(const int32_t *in, int32_t *out, i
     return __shfl_sync(0xFFFFFFFFu, incl, 31);
 }
 
+// The dispatch plan: from the expert counts of every 128-token block, the
+// experts' totals, exclusive receive offsets (expert-major, then token), each
+// block's base row per expert and each rank's row-block units.  By one group
+// of NUM_EPI_THREADS threads (et) with named barrier 1, once every block's
+// counts are visible; scr: 8 KB of shared memory.
+struct MoePlanOut {
+    int32_t *blk_counts;
+    int32_t *base, *offsets, *offl, *counts, *counts_out, *unit_start;
+};
+__device__ __forceinline__ void moe_plan(const MoePlanOut &o, const MoeGeom &g, int et, uint8_t *escr) {
+    const int E = g.E;
+    int32_t *s_cnt = reinterpret_cast<int32_t *>(escr + 5120);
+    int32_t *s_off = reinterpret_cast<int32_t *>(escr + 6144);
+    for (int i = et; i < E; i += NUM_EPI_THREADS) {
+        int c = 0;
+#pragma unroll 8
+        for (int gb = 0; gb < g.NB; ++gb) c += ldcg_i32(&o.blk_counts[gb * E + i]);
+        s_cnt[i] = c;
+        o.counts[i] = c;
+        o.counts_out[i] = c;
+    }
+    named_bar_sync(1, NUM_EPI_THREADS);
+    // exclusive prefix sums by warp scans (a serial loop interleaving shared
+    // and global accesses cost tens of microseconds here): warp 0 scans the
+    // expert counts into the receive offsets, warps 1.. scan each rank's
+    // row-block units
+    int32_t *s_us = reinterpret_cast<int32_t *>(escr);           // [P][Eq + 1] <= 264 words, over s_bits (done with)
+    int32_t *s_offl = reinterpret_cast<int32_t *>(escr + 2048);  // [E + 1], MXFP8 only, over s_bits
+    const int ew = et / 32, lane = et % 32;
+    if (ew == 0) {
+        if (g.mx) {
+            // receive offsets without padding (reported), and with every expert
+            // starting on a 128-row boundary (the layout of the buffers)
+            const int tl = warp_excl_scan(s_cnt, s_offl, E, lane, 0);
+            if (lane == 0) s_offl[E] = tl;
+            const int tu = warp_excl_scan(s_cnt, s_off, E, lane, BM);
+            __syncwarp();
+            for (int i = lane; i < E; i += 32) s_off[i] *= BM;
+            if (lane == 0) s_off[E] = tu * BM;
+        } else {
+            const int total = warp_excl_scan(s_cnt, s_off, E, lane, 0);
+            if (lane == 0) s_off[E] = total;
+        }
+    } else {
+        for (int qq = ew - 1; qq < g.P; qq += NUM_EPI_THREADS / 32 - 1) {
+            const int total = warp_excl_scan(s_cnt + qq * g.Eq, s_us + qq * (g.Eq + 1), g.Eq, lane, BM);
+            if (lane == 0) s_us[qq * (g.Eq + 1) + g.Eq] = total;
+        }
+    }
+    named_bar_sync(1, NUM_EPI_THREADS);
+    for (int i = et; i <= E; i += NUM_EPI_THREADS) {
+        o.offsets[i] = s_off[i];
+        o.offl[i] = g.mx ? s_offl[i] : s_off[i];
+    }
+    for (int i = et; i < g.P * (g.Eq + 1); i += NUM_EPI_THREADS) o.unit_start[i] = s_us[i];
+    for (int i = et; i < E; i += NUM_EPI_THREADS) {
+        int run = s_off[i];
+#pragma unroll 8
+        for (int gb = 0; gb < g.NB; ++gb) {
+            o.base[gb * E + i] = run;
+            run += ldcg_i32(&o.blk_counts[gb * E + i]);
+        }
+    }
+    __threadfence();
+    named_bar_sync(1, NUM_EPI_THREADS);
+}
+
+struct MoePlanLaunch {
+    MoeGeom g;
+    const int32_t *idx;
+    WsHeader *ws;
+    uint32_t *route_done;
+    int32_t *rank_in_blk;
+    float *logits;
+    MoePlanOut out;
+};
+kosmos_status launch_moe_plan(const MoePlanLaunch &L, cudaStream_t stream);
+
 // fp32 silu through the fast exponential and the approximate division (a
 // few ulp; h is rounded to bf16 or quantised to E4M3 after it): the
 // correctly rounded division took a large share of the SwiGLU epilogue

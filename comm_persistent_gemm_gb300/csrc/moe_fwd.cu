@@ -93,7 +93,8 @@ struct MoeParams {
     MoeGeom g;
     int fold_tps;                    // FOLD: tokens per pipeline stage (64 / K)
     int phase;                       // 0: the whole layer in this launch; 1-5: one phase of the unfused
-                                     // baseline (ROUTE+PLAN[+QUANT] | DISPATCH | TILE_GU | TILE_D | PUSH+FOLD)
+                                     // baseline (ROUTE+PLAN[+QUANT] | DISPATCH | TILE_GU | TILE_D | PUSH+FOLD);
+                                     // 6: the layer from DISPATCH on, routing and plan given (moe_routed.cu)
     uint64_t wait_limit_ns;
     uint64_t inject;
 };
@@ -208,10 +209,12 @@ __device__ __forceinline__ int moe_decide(const MoeParams &p, const Smem &sm, Mo
     // main-rail tickets: one counter per rank; a phase of the unfused baseline
     // counts from its own first ticket (the counters start from zero in
     // every launch)
-    const uint32_t base = ph == 2 ? static_cast<uint32_t>(g.RB + g.NQ) : (ph >= 3 ? static_cast<uint32_t>(g.n_head) : 0u);
+    const bool whole = ph == 0 || ph == 6;
+    const uint32_t base = ph == 2 || ph == 6 ? static_cast<uint32_t>(g.RB + g.NQ)
+                                             : (ph >= 3 ? static_cast<uint32_t>(g.n_head) : 0u);
     uint32_t *tctr = &p.ws->tickets[q];
     // 1) a ready result to push back to its source rank
-    if (st.plan_seen && (ph == 0 || ph == 5)) {
+    if (st.plan_seen && (whole || ph == 5)) {
         int32_t code;
         if (queue_try_take(&qc[1], &qc[0], p.push_items + q * g.push_cap, p.push_flags + q * g.push_cap, epoch,
                            code, p.ws)) {
@@ -311,7 +314,7 @@ __device__ __forceinline__ int moe_decide(const MoeParams &p, const Smem &sm, Mo
         moe_decode_tile(p, st.us, tt, kind, le, rb, col);
         if (kind == 0) {
             st.main_done = true;
-            if (ph != 0) return ACT_EXIT;
+            if (!whole) return ACT_EXIT;
         } else if ((ph == 3 && kind != K_TILE_GU) || (ph == 4 && kind != K_TILE_D)) {
             st.ahead = base + atomicAdd(tctr, 1u);  // another phase's tile: take the next ticket
             return ACT_NONE;
@@ -406,7 +409,7 @@ __device__ __forceinline__ int moe_decide(const MoeParams &p, const Smem &sm, Mo
         }
     }
     // 3) a ready fold of this rank's tokens
-    if (st.plan_seen && (ph == 0 || ph == 5)) {
+    if (st.plan_seen && (whole || ph == 5)) {
         int32_t code;
         if (queue_try_take(&qc[3], &qc[2], p.fold_items + q * g.fold_cap, p.fold_flags + q * g.fold_cap, epoch, code,
                            p.ws)) {
@@ -705,60 +708,7 @@ __device__ __noinline__ void moe_route_epilogue(const MoeParams &p, const SchedE
     if (*s_last == 0) return;
     // PLAN: every route block has published its counts
     __threadfence();
-    int32_t *s_cnt = reinterpret_cast<int32_t *>(escr + 5120);
-    int32_t *s_off = reinterpret_cast<int32_t *>(escr + 6144);
-    for (int i = et; i < E; i += NUM_EPI_THREADS) {
-        int c = 0;
-#pragma unroll 8
-        for (int gb = 0; gb < g.NB; ++gb) c += ldcg_i32(&p.blk_counts[gb * E + i]);
-        s_cnt[i] = c;
-        p.counts[i] = c;
-        p.counts_out[i] = c;
-    }
-    named_bar_sync(1, NUM_EPI_THREADS);
-    // exclusive prefix sums by warp scans (a serial loop interleaving shared
-    // and global accesses cost tens of microseconds here): warp 0 scans the
-    // expert counts into the receive offsets, warps 1.. scan each rank's
-    // row-block units
-    int32_t *s_us = reinterpret_cast<int32_t *>(escr);           // [P][Eq + 1] <= 264 words, over s_bits (done with)
-    int32_t *s_offl = reinterpret_cast<int32_t *>(escr + 2048);  // [E + 1], MXFP8 only, over s_bits
-    const int ew = et / 32, lane = et % 32;
-    if (ew == 0) {
-        if (g.mx) {
-            // receive offsets without padding (reported), and with every expert
-            // starting on a 128-row boundary (the layout of the buffers)
-            const int tl = warp_excl_scan(s_cnt, s_offl, E, lane, 0);
-            if (lane == 0) s_offl[E] = tl;
-            const int tu = warp_excl_scan(s_cnt, s_off, E, lane, BM);
-            __syncwarp();
-            for (int i = lane; i < E; i += 32) s_off[i] *= BM;
-            if (lane == 0) s_off[E] = tu * BM;
-        } else {
-            const int total = warp_excl_scan(s_cnt, s_off, E, lane, 0);
-            if (lane == 0) s_off[E] = total;
-        }
-    } else {
-        for (int qq = ew - 1; qq < g.P; qq += NUM_EPI_THREADS / 32 - 1) {
-            const int total = warp_excl_scan(s_cnt + qq * g.Eq, s_us + qq * (g.Eq + 1), g.Eq, lane, BM);
-            if (lane == 0) s_us[qq * (g.Eq + 1) + g.Eq] = total;
-        }
-    }
-    named_bar_sync(1, NUM_EPI_THREADS);
-    for (int i = et; i <= E; i += NUM_EPI_THREADS) {
-        p.offsets[i] = s_off[i];
-        p.offl[i] = g.mx ? s_offl[i] : s_off[i];
-    }
-    for (int i = et; i < g.P * (g.Eq + 1); i += NUM_EPI_THREADS) p.unit_start[i] = s_us[i];
-    for (int i = et; i < E; i += NUM_EPI_THREADS) {
-        int run = s_off[i];
-#pragma unroll 8
-        for (int gb = 0; gb < g.NB; ++gb) {
-            p.base[gb * E + i] = run;
-            run += ldcg_i32(&p.blk_counts[gb * E + i]);
-        }
-    }
-    __threadfence();
-    named_bar_sync(1, NUM_EPI_THREADS);
+    moe_plan({p.blk_counts, p.base, p.offsets, p.offl, p.counts, p.counts_out, p.unit_start}, g, et, escr);
     if (et == 0) st_release_gpu(&p.ws->aux[1], epoch + 1u);
 }
 
@@ -1344,7 +1294,7 @@ kosmos_status launch_moe_fwd(const MoeLaunch &Lc, cudaStream_t stream) {
                 return KOSMOS_ERR_CUDA;
         }
     }
-    {
+    if (!Lc.routed) {
         const uint64_t dims[2] = {E, H};
         const uint64_t st[1] = {E * 2};
         const uint32_t box[2] = {64, BK};
@@ -1386,6 +1336,19 @@ kosmos_status launch_moe_fwd(const MoeLaunch &Lc, cudaStream_t stream) {
         if (!encode_tmap(&p.tmSlot, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.slot, dims, st, box,
                          CU_TENSOR_MAP_SWIZZLE_NONE))
             return KOSMOS_ERR_CUDA;
+    }
+    if (Lc.routed) {
+        MoePlanLaunch pl;
+        pl.g = g;
+        pl.idx = Lc.topk_idx;
+        pl.ws = p.ws;
+        pl.route_done = p.route_done;
+        pl.rank_in_blk = p.rank_in_blk;
+        pl.logits = p.logits;
+        pl.out = {p.blk_counts, p.base, p.offsets, p.offl, p.counts, p.counts_out, p.unit_start};
+        const kosmos_status st = launch_moe_plan(pl, stream);
+        if (st != KOSMOS_OK) return st;
+        p.phase = 6;
     }
     if (Lc.sched != KOSMOS_SCHED_UNFUSED)
         return launch_persistent(reinterpret_cast<const void *>(&moe_fwd_kernel), &p, Lc.grid, MOE_SMEM_BYTES, stream,

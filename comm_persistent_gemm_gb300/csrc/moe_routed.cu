@@ -1,0 +1,90 @@
+// moe_routed.cu -- the dispatch plan of a given routing: what the expert layer's
+// ROUTE entries leave behind, from topk_idx instead of the layer's own router,
+// so that the fused kernel can run from its DISPATCH entries on.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "moe_common.cuh"
+#include "launch.h"
+
+namespace kosmos {
+
+// One block per 128 tokens of a rank, one token per thread: each slot's rank
+// among the block's slots of the same expert, and the block's expert counts;
+// the last block to finish makes the plan.  A token whose experts are not
+// topk different ones in [0, E) ends the call with INVALID_ARG and the token in
+// the status (the fused kernel then leaves at once); its slots are left out,
+// so nothing is written out of range.
+__global__ void __launch_bounds__(NUM_EPI_THREADS) moe_plan_kernel(const __grid_constant__ MoePlanLaunch p) {
+    __shared__ __align__(16) uint8_t s_scr[8192];
+    __shared__ int s_last;
+    const MoeGeom &g = p.g;
+    const int E = g.E, K = g.K, et = threadIdx.x, gb = blockIdx.x;
+    const int q = gb / g.RB, b = gb % g.RB;
+    const int64_t tl = static_cast<int64_t>(b) * BM + et;
+    const int64_t t0 = static_cast<int64_t>(q) * g.Tq + static_cast<int64_t>(b) * BM;
+    const int64_t left = g.Tq - static_cast<int64_t>(b) * BM;
+    const int rows = static_cast<int>(left < BM ? left : BM);
+    uint32_t *s_bits = reinterpret_cast<uint32_t *>(s_scr);  // [E][4]: bit r of an expert's 128: token r has it
+    for (int i = et; i < 4 * E; i += NUM_EPI_THREADS) s_bits[i] = 0u;
+    // the backward reads the saved logits; a given routing has none: zeros
+    float4 *lg = reinterpret_cast<float4 *>(p.logits + t0 * E);
+    for (int i = et; i < rows * E / 4; i += NUM_EPI_THREADS) lg[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    int ti[MOE_MAXK];
+    bool valid = tl < g.Tq;
+    const int64_t t = t0 + et;
+    if (valid) {
+        uint32_t seen[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};  // one bit per expert (E <= 256)
+        bool ok = true;
+#pragma unroll
+        for (int k = 0; k < MOE_MAXK; ++k) {
+            ti[k] = k < K ? p.idx[t * K + k] : 0;
+            if (k >= K) continue;
+            if (ti[k] < 0 || ti[k] >= E) {
+                ok = false;
+                continue;
+            }
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+                if (w == (ti[k] >> 5)) {
+                    if ((seen[w] >> (ti[k] & 31)) & 1u) ok = false;
+                    seen[w] |= 1u << (ti[k] & 31);
+                }
+        }
+        if (!ok) {
+            set_error(p.ws, KOSMOS_ERR_INVALID_ARG, t);
+            valid = false;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < MOE_MAXK; ++k)
+        if (valid && k < K) atomicOr(&s_bits[4 * ti[k] + (et >> 5)], 1u << (et & 31));
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < MOE_MAXK; ++k)
+        if (valid && k < K) {
+            const uint32_t *b4 = s_bits + 4 * ti[k];
+            int rk = __popc(b4[et >> 5] & ((1u << (et & 31)) - 1u));
+            for (int w = 0; w < (et >> 5); ++w) rk += __popc(b4[w]);
+            p.rank_in_blk[t * K + k] = rk;
+        }
+    int32_t *blk = p.out.blk_counts + static_cast<int64_t>(gb) * E;
+    for (int i = et; i < E; i += NUM_EPI_THREADS)
+        blk[i] = __popc(s_bits[4 * i]) + __popc(s_bits[4 * i + 1]) + __popc(s_bits[4 * i + 2]) + __popc(s_bits[4 * i + 3]);
+    __threadfence();
+    __syncthreads();
+    if (et == 0) s_last = atom_add_acqrel_gpu(p.route_done, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    moe_plan(p.out, g, et, s_scr);
+    if (et == 0) st_release_gpu(&p.ws->aux[1], *reinterpret_cast<volatile uint32_t *>(&p.ws->epoch) + 1u);
+}
+
+kosmos_status launch_moe_plan(const MoePlanLaunch &L, cudaStream_t stream) {
+    moe_plan_kernel<<<L.g.NB, NUM_EPI_THREADS, 0, stream>>>(L);
+    return cudaGetLastError() == cudaSuccess ? KOSMOS_OK : KOSMOS_ERR_CUDA;
+}
+
+}  // namespace kosmos

@@ -286,6 +286,31 @@ KOSMOS_API kosmos_status kosmos_moe_fwd(const void *const *x_shards, const void 
                              int32_t *dispatch_pos, void *ws, size_t ws_bytes,
                              const kosmos_opts *opts, void *stream);
 
+/*
+ * The same layer on a given routing (BF16): the dispatch plan of topk_idx in
+ * one short launch, then the layer's launch from the dispatch on.  For layers
+ * with another router than the softmax top-K: kosmos_route makes topk_idx and
+ * topk_gate, kosmos_route_bwd takes their gradient on.
+ *
+ *   topk_idx, topk_gate : [tokens, topk] int32 and fp32, given.  Every token
+ *                   needs topk different experts in [0, n_experts); one that has not
+ *                   ends the call with KOSMOS_ERR_INVALID_ARG in the workspace
+ *                   status, the token as its entry, and no output.
+ *   the rest        as for kosmos_moe_fwd (expert_counts and dispatch_pos are
+ *                   outputs), same workspace.  SELF schedule, no injection.
+ *
+ * Its backward is kosmos_moe_bwd on this call's workspace, topk_idx and topk_gate with a
+ * w_router of zeros: dx is then the experts' part alone, the gates' gradient
+ * is view 5 of kosmos_moe_bwd_debug_view, and dw_router is to be ignored (the
+ * workspace holds logits of zero).
+ */
+KOSMOS_API kosmos_status kosmos_moe_fwd_routed(const void *const *x_shards, int P, int64_t tokens, int64_t hidden,
+                             int n_experts, int topk, int64_t inter, const void *const *w_gate,
+                             const void *const *w_up, const void *const *w_down, const int32_t *topk_idx,
+                             const float *topk_gate, void *const *y_shards, int32_t *expert_counts,
+                             int32_t *dispatch_pos, void *ws, size_t ws_bytes, const kosmos_opts *opts,
+                             void *stream);
+
 /* Workspace size in bytes for kosmos_moe_fwd with these sizes and dtype (opts
  * may be NULL).  Returns 0 for invalid sizes or dtype. */
 KOSMOS_API size_t kosmos_moe_workspace_bytes(int P, int64_t tokens, int64_t hidden, int n_experts, int topk,

@@ -119,6 +119,28 @@ def test_grad_refuses(K, base):
     assert norm([4], [0], ws=base + 4) == K.ERR_WORKSPACE
 
 
+def test_moe_fwd_routed_refuses(K, base):
+    L = K.lib()
+    P, T, H, E, k, I = 2, 128, 256, 64, 4, 128
+    ptr = (C.c_void_p * P)(base, base)
+    bad = (C.c_void_p * P)(base, base + 2)
+
+    def call(x=ptr, P=P, T=T, H=H, E=E, k=k, I=I, wg=ptr, wu=ptr, wd=ptr, idx=base, gate=base, y=ptr, cnt=base, pos=base,
+             ws=base, nb=1 << 40, o=None):
+        return L.kosmos_moe_fwd_routed(x, P, T, H, E, k, I, wg, wu, wd, idx, gate, y, cnt, pos, ws, nb,
+                                       C.byref(o) if o else None, None)
+
+    for kw in (dict(P=0), dict(P=3), dict(T=127), dict(H=100), dict(E=60), dict(E=512), dict(k=0), dict(k=9), dict(I=100),
+               dict(x=None), dict(x=bad), dict(wg=None), dict(wu=bad), dict(wd=None), dict(idx=None), dict(idx=base + 4),
+               dict(gate=None), dict(y=bad), dict(cnt=None), dict(pos=base + 8)):
+        assert call(**kw) == K.ERR_INVALID_ARG, kw
+    for kw in (dict(ws=None), dict(ws=base + 8), dict(nb=1024)):
+        assert call(**kw) == K.ERR_WORKSPACE, kw
+    for kw in (dict(sched=K.SCHED_UNFUSED), dict(sched=K.SCHED_FIXED), dict(inject=K.INJECT_IDENTITY_EXPERTS),
+               dict(link_gbs=100)):
+        assert call(o=K.opts(**kw)) == K.ERR_UNSUPPORTED, kw
+
+
 def test_binding_refuses(K):
     """The binding's own checks: CPU tensors, types, shapes, strides."""
     x, r = torch.zeros(4, 8), K.router(topk=2)
