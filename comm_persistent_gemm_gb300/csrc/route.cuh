@@ -71,26 +71,50 @@ __device__ __forceinline__ float rcp(float x) {
 template <typename T, int L, int V> struct Layout {
     static constexpr int W = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
     static __device__ __forceinline__ int expert(int l, int v) { return (v / W) * L * W + l * W + v % W; }
-    // the values as floats; beyond E: -inf
-    static __device__ __forceinline__ void load(const T *row, int E, int l, bool vec, float *x) {
+    // The values as floats, beyond E -inf.  Returns a sum that is 0 if the
+    // values within E are finite and NaN if not (the multiply-adds are cheap
+    // here, comparisons and selections are what the kernels are bound by).
+    static __device__ __forceinline__ float load(const T *row, int E, int l, bool vec, float *x) {
+        static_assert(W * sizeof(T) >= 8, "a piece is 8 or 16 bytes");
+        constexpr int NW = W * sizeof(T) / 4;  // words of a piece
+        float odd = 0.f;
+        if (vec) {
+            uint32_t r[V / W][NW];
 #pragma unroll
-        for (int c = 0; c < V; c += W) {
-            const int e0 = expert(l, c);
-            alignas(16) T r[W];
-            if (vec) {
-                if (e0 < E) {
-                    if constexpr (W * sizeof(T) == 16)
-                        *reinterpret_cast<uint4 *>(r) = *reinterpret_cast<const uint4 *>(row + e0);
-                    else
-                        *reinterpret_cast<uint2 *>(r) = *reinterpret_cast<const uint2 *>(row + e0);
-                    static_assert(W * sizeof(T) >= 8, "a piece is 8 or 16 bytes");
-                }
+            for (int c = 0; c < V / W; ++c) load_piece(r[c], row + expert(l, c * W), expert(l, c * W) < E);
 #pragma unroll
-                for (int i = 0; i < W; ++i) x[c + i] = e0 < E ? to_f32(r[i]) : -INFINITY;
-            } else {
-#pragma unroll
-                for (int i = 0; i < W; ++i) x[c + i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
+            for (int v = 0; v < V; ++v) {
+                const float f = to_f32(reinterpret_cast<const T *>(r[v / W])[v % W]);
+                const bool in = expert(l, v - v % W) < E;
+                odd = fmaf(f, 0.f, odd);  // 0 beyond E
+                x[v] = in ? f : -INFINITY;
             }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[v] = expert(l, v) < E ? to_f32(row[expert(l, v)]) : 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                odd = fmaf(x[v], 0.f, odd);
+                if (expert(l, v) >= E) x[v] = -INFINITY;
+            }
+        }
+        return odd;
+    }
+    // In order and unconditionally issued, so that a row's pieces are all on
+    // their way before the first is used; zeros where not `in`.
+    static __device__ __forceinline__ void load_piece(uint32_t *r, const T *p, bool in) {
+        if constexpr (W * sizeof(T) == 16) {
+            r[0] = r[1] = r[2] = r[3] = 0u;
+            asm volatile("{ .reg .pred q; setp.ne.s32 q, %5, 0; @q ld.global.v4.u32 {%0, %1, %2, %3}, [%4]; }"
+                         : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])
+                         : "l"(p), "r"(static_cast<int>(in))
+                         : "memory");
+        } else {
+            r[0] = r[1] = 0u;
+            asm volatile("{ .reg .pred q; setp.ne.s32 q, %3, 0; @q ld.global.v2.u32 {%0, %1}, [%2]; }"
+                         : "+r"(r[0]), "+r"(r[1])
+                         : "l"(p), "r"(static_cast<int>(in))
+                         : "memory");
         }
     }
 };

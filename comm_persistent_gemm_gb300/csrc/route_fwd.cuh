@@ -19,7 +19,7 @@ namespace {
 constexpr int ROUTE_WARPS = 8;
 constexpr int ROUTE_THREADS = ROUTE_WARPS * 32;
 #ifndef MINB
-#define MINB 2
+#define MINB 3
 #endif
 #ifndef SMT
 #define SMT 16
@@ -107,14 +107,19 @@ __device__ __forceinline__ float difference(dd a, dd b) { return (a.hi - b.hi) +
 // A lane's best D keys in order.  A key's low bits hold the expert (as
 // MASK - e: the lower expert first), so keys differ and a maximum tells
 // whose it is; a value's own low bits are lost, which matters to fp32 values
-// only (a bf16 or fp16 value has at least 13 zero bits).  Four are enough for
-// eight choices from eight lanes in 99 of 100 rows, two for as many from 32
-// lanes in 93; a lane that has given its list away makes the next one.
+// only (a bf16 or fp16 value has at least 13 zero bits).  A lane that has given
+// its list away makes the next one: of eight choices from eight lanes some lane
+// gives four in 13 rows of 100 and five in 2, from 32 lanes two in 60, four
+// in 0.2.
 template <int L, int V> struct Best {
-    static constexpr int D = L == 32 && V > 4 ? 2 : 4;
+    static constexpr int D = L == 32 && V > 4 ? 3 : V > 8 ? 5 : 4;
     static constexpr uint32_t MASK = L * V - 1;
     uint32_t k[D];
-    static __device__ __forceinline__ uint32_t key_of(float f, int e) { return (float_key(f) & ~MASK) | (MASK - e); }
+    // low: MASK - e for a lane's v = 0; the others' differ from it in v's bits alone
+    static __device__ __forceinline__ uint32_t key_of(float f, uint32_t low, uint32_t v_bits) {
+        return ((float_key(f) & ~MASK) | low) ^ v_bits;
+    }
+    static __device__ __forceinline__ uint32_t closed(uint32_t key) { return (key & MASK) | (KEY_CLOSED & ~MASK); }
     static __device__ __forceinline__ int expert(uint32_t key) { return static_cast<int>(MASK - (key & MASK)); }
     static __device__ __forceinline__ bool is_open(uint32_t key) { return (key | MASK) > KEY_CLOSED; }
     __device__ __forceinline__ void insert(uint32_t x) {
@@ -519,21 +524,22 @@ __global__ void __launch_bounds__(ROUTE_THREADS, MINB) route_kernel(const __grid
             const bool live = t0 + seg < p.T;
             const T *row = logits + (live ? t0 + seg : t0) * p.ld;
             float s[V];
-            Lay::load(row, p.E, l, p.vec, s);
+            const float odd = Lay::load(row, p.E, l, p.vec, s);
             bool nan = false;
             float m = 0.f, z = 1.f;
+            if (__any_sync(FULL, odd != 0.f)) {  // NaN or infinite logits
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                nan = nan || s[v] != s[v];
-                if (MODE != BY_SIGMOID) s[v] = fmaxf(s[v], -INFINITY);  // NaN: closed
+                for (int v = 0; v < V; ++v) {
+                    nan = nan || s[v] != s[v] || (softmax && s[v] == INFINITY);
+                    s[v] = fmaxf(s[v], -INFINITY);  // NaN: closed
+                }
+                nan = (__ballot_sync(FULL, nan) >> (seg * L) & ROW) != 0u;
             }
             if (softmax) {
                 m = s[0];
 #pragma unroll
                 for (int v = 1; v < V; ++v) m = fmaxf(m, s[v]);
-                nan = nan || m == INFINITY;
             }
-            nan = (__ballot_sync(FULL, nan) >> (seg * L) & ROW) != 0u;
             // s: what orders the experts and scores the groups; closed experts -inf
             float rz = 1.f;
             if (need_z) {
@@ -550,6 +556,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, MINB) route_kernel(const __grid
                 rz = rcp(z);
             }
             uint32_t key[V];
+            const uint32_t low = MASK - Lay::expert(l, 0);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int e = Lay::expert(l, v);
@@ -558,15 +565,22 @@ __global__ void __launch_bounds__(ROUTE_THREADS, MINB) route_kernel(const __grid
                     const float q = MODE == BY_SOFTMAX ? s[v] * rz : fast_sigmoid(s[v]);
                     s[v] = s[v] > -INFINITY ? fmaxf(q + b, -INFINITY) : -INFINITY;
                 }
-                key[v] = List::key_of(s[v], e);
+                key[v] = List::key_of(s[v], low, Lay::expert(0, v));
             }
             bool near = false;
             if (p.GK < p.G) {
                 const uint32_t open = open_groups<T, L, V, MODE>(p, row, s, s_row, l, seg, m, rz, near);
+                if (p.gs % 4 == 0) {  // four consecutive experts are of one group
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int e = Lay::expert(l, v);
-                    if (!((open >> (((e * p.gmul) >> 20) & 31)) & 1u)) key[v] = List::key_of(-INFINITY, e);
+                    for (int v = 0; v < V; v += 4)
+                        if (!((open >> (((Lay::expert(l, v) * p.gmul) >> 20) & 31)) & 1u)) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) key[v + i] = List::closed(key[v + i]);
+                        }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (!((open >> (((Lay::expert(l, v) * p.gmul) >> 20) & 31)) & 1u)) key[v] = List::closed(key[v]);
                 }
             }
             List list;
@@ -627,11 +641,14 @@ __global__ void __launch_bounds__(ROUTE_THREADS, MINB) route_kernel(const __grid
 #pragma unroll
             for (int h = 0; h < N; ++h) {
                 const bool mine = my_key[h] != KEY_NONE;
+                my_g[h] = 0.f;
                 my_open[h] = mine && List::is_open(my_key[h]);
                 my_e[h] = mine ? List::expert(my_key[h]) : 0;
                 rank[h] = mine ? h * L + l : p.k;
+                my_x[h] = 0.f;
+                if (h * L >= most) continue;
                 if (EXACT) my_x[h] = key_float((my_key[h] & 0x80000000u) ? my_key[h] & ~MASK : my_key[h] | MASK);
-                else my_x[h] = h * L < most ? to_f32(row[my_e[h]]) : 0.f;
+                else my_x[h] = to_f32(row[my_e[h]]);
             }
             if (!EXACT) {
                 // ranked by the score in full; equal scores keep the keys' order,
@@ -640,24 +657,40 @@ __global__ void __launch_bounds__(ROUTE_THREADS, MINB) route_kernel(const __grid
                 bool close = false;
 #pragma unroll
                 for (int h = 0; h < N; ++h) {
+                    my_s[h] = -INFINITY;
+                    my_b[h] = my_err[h] = 0.f;
+                    if (h * L >= most) continue;
                     my_b[h] = MODE != BY_LOGIT && p.bias != nullptr ? __ldg(p.bias + my_e[h]) : 0.f;
                     const float q = MODE == BY_SOFTMAX ? fast_softmax(my_x[h], m, rz) : fast_sigmoid(my_x[h]);
                     my_s[h] = !my_open[h] ? -INFINITY : MODE == BY_LOGIT ? my_x[h] : q + my_b[h];
                     my_err[h] = MODE == BY_LOGIT || !my_open[h] ? 0.f : score_error(MODE == BY_SOFTMAX, my_s[h], q, rz);
-                    if (my_key[h] != KEY_NONE) rank[h] = 0;
                 }
+                // in order already, as the keys are, unless some neighbours are not
+                // apart: compared with the next slot's score
+                bool apart = most <= L;
+                if (most <= L) {
+                    const float s2 = __shfl_down_sync(FULL, my_s[0], 1);
+                    const float err2 = MODE == BY_LOGIT ? 0.f : __shfl_down_sync(FULL, my_err[0], 1);
+                    apart = l >= most - 1 || l == L - 1 || s2 == -INFINITY || my_s[0] - s2 > my_err[0] + err2;
+                }
+                if (!__all_sync(FULL, apart)) {
 #pragma unroll
-                for (int ho = 0; ho < N; ++ho)
-                    for (int o = 0; o < L && ho * L + o < most; ++o) {
-                        const float so = __shfl_sync(FULL, my_s[ho], seg * L + o);
+                    for (int h = 0; h < N; ++h)
+                        if (my_key[h] != KEY_NONE) rank[h] = 0;
 #pragma unroll
-                        for (int h = 0; h < N; ++h) {
-                            const int me = h * L + l, it = ho * L + o;
-                            rank[h] += (so > my_s[h] || (so == my_s[h] && it < me)) ? 1 : 0;
-                            // a pair within its errors: the wider one's is at least half of their sum
-                            if (MODE != BY_LOGIT) close = close || (it != me && fabsf(so - my_s[h]) <= 2.f * my_err[h]);
+                    for (int ho = 0; ho < N; ++ho)
+                        for (int o = 0; o < L && ho * L + o < most; ++o) {
+                            const float so = __shfl_sync(FULL, my_s[ho], seg * L + o);
+#pragma unroll
+                            for (int h = 0; h < N; ++h) {
+                                const int me = h * L + l, it = ho * L + o;
+                                rank[h] += (so > my_s[h] || (so == my_s[h] && it < me)) ? 1 : 0;
+                                // a pair within its errors: the wider one's is at least half of their sum
+                                if (MODE != BY_LOGIT)
+                                    close = close || (it != me && fabsf(so - my_s[h]) <= 2.f * my_err[h]);
+                            }
                         }
-                    }
+                }
                 if (MODE != BY_LOGIT && __any_sync(FULL, close)) {
                     const dd drz = MODE == BY_SOFTMAX ? row_inverse_z<T, L, V>(row, p.E, l, p.vec, m) : dd{1.f, 0.f};
                     dd my_d[N];
@@ -700,7 +733,8 @@ __global__ void __launch_bounds__(ROUTE_THREADS, MINB) route_kernel(const __grid
             }
 #pragma unroll
             for (int h = 0; h < N; ++h) my_open[h] = my_open[h] && rank[h] < p.k;
-            route_gates<L, N>(p, my_x, my_open, m, z, my_g);
+            if (N == 1 || most <= L) route_gates<L, 1>(p, my_x, my_open, m, z, my_g);
+            else route_gates<L, N>(p, my_x, my_open, m, z, my_g);
 #pragma unroll
             for (int h = 0; h < N; ++h)
                 if (live && rank[h] < p.k) {
@@ -761,7 +795,10 @@ kosmos_status launch_route_v(const RouteParams &q, int sms, cudaStream_t stream)
     while (warps > 1 && 4ll * (p.hist_words + warps * R * p.row_words) > 40960) warps /= 2;
     const size_t smem = 4ull * (p.hist_words + warps * R * p.row_words);
     int64_t blocks = cdiv(p.T, R * warps);
-    const int64_t most = static_cast<int64_t>(MINB) * (ROUTE_WARPS / warps) * sms;
+#ifndef BPM
+#define BPM 1
+#endif
+    const int64_t most = static_cast<int64_t>(BPM) * MINB * (ROUTE_WARPS / warps) * sms;
     if (blocks > most) blocks = most;
     return launch_overlapped(&route_kernel<T, L, V, MODE>, static_cast<unsigned>(blocks), warps * 32, smem, stream, p);
 }
@@ -772,8 +809,14 @@ template <typename T, int MODE> kosmos_status launch_route_m(const RouteParams &
         return p.E <= 128 ? launch_route_v<T, 32, 4, MODE>(p, sms, stream) : launch_route_v<T, 32, 8, MODE>(p, sms, stream);
     if (p.E <= 32) return launch_route_v<T, 8, 4, MODE>(p, sms, stream);
     if (p.E <= 64) return launch_route_v<T, 8, 8, MODE>(p, sms, stream);
-    if (p.E <= 128) return launch_route_v<T, 8, 16, MODE>(p, sms, stream);
-    if (p.E <= 256) return launch_route_v<T, 8, 32, MODE>(p, sms, stream);
+#ifndef LA
+#define LA 8
+#endif
+#ifndef LB
+#define LB 8
+#endif
+    if (p.E <= 128) return launch_route_v<T, LA, 128 / LA, MODE>(p, sms, stream);
+    if (p.E <= 256) return launch_route_v<T, LB, 256 / LB, MODE>(p, sms, stream);
     if (p.E <= 512) return launch_route_v<T, 16, 32, MODE>(p, sms, stream);
     return launch_route_v<T, 32, 32, MODE>(p, sms, stream);
 }
