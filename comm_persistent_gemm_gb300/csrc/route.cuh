@@ -24,9 +24,10 @@ struct RouteParams {
     int E, k, G, GK, group_top, score, renorm;
     float scale;
     // set by the launcher
-    bool vec;                         // pieces of a row are loaded whole
-    int hist_words, row_words;        // shared memory: counts, then a row of values (groups only)
-    int gs, gsp, gmul;                // group size, its stride in shared memory, division by gs
+    bool vec;                         // rows are loaded in 16-byte pieces
+    int width, warp_words;            // shared memory: a row's values, a warp's rows
+    uint32_t mask;                    // the bits of a key that hold the expert
+    int gs, gmul;                     // group size, division by it
 };
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -44,6 +45,7 @@ template <int L> __device__ __forceinline__ float row_max(float v) {
     return v;
 }
 template <int L> __device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    if (L == 32) return __reduce_max_sync(FULL, v);
 #pragma unroll
     for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(FULL, v, d));
     return v;

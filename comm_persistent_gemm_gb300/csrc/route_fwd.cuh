@@ -5,9 +5,14 @@
 // translation unit per type of logits instantiates it.
 //
 // L lanes of a warp share a row (8 up to 256 experts, so that a warp orders
-// four rows at once), each with V of its values.  The choice is k rounds of
+// four rows at once); its values wait in shared memory.  The choice is k rounds of
 // a maximum over the lanes; what decides it is an order in which ties go to
 // the lower expert, so the result is a function of the row alone.
+//
+// The loops over a row's values are kept rolled: with them unrolled, values
+// in registers, the kernel was 30 KB of instructions, which every SM fetches in
+// every launch and no instruction cache close to the schedulers holds (a quarter
+// of the issue slots lost at 32768 x 256, 5 us of the time of few rows).
 #pragma once
 #include "dd.cuh"
 #include "route.cuh"
@@ -18,10 +23,14 @@ namespace {
 
 constexpr int ROUTE_WARPS = 8;
 constexpr int ROUTE_THREADS = ROUTE_WARPS * 32;
-// Blocks per SM that the registers are made to fit: a lane with up to eight
-// values runs as well in 64 (40009 x 60: 9.8 us, 11.0 us in 80), one with 16 or
-// 32 in 80 (32768 x 256: 32 us, 38 us in 128).
-constexpr int route_blocks(int V) { return V <= 8 ? 4 : 3; }
+#ifndef UN
+#define UN 2
+#endif
+#ifndef RB
+#define RB 5
+#endif
+constexpr int LIST_UNROLL = UN;
+constexpr int ROUTE_BLOCKS = RB;      // per SM, which the registers are made to fit
 #ifndef SMT
 #define SMT 20
 #endif
@@ -37,30 +46,32 @@ template <int L> constexpr uint32_t row_lanes() { return L == 32 ? FULL : (1u <<
 template <int L, int N>
 __device__ __forceinline__ void route_gates(const RouteParams &p, const float *x, const bool *open, float m, float z,
                                             float *g) {
+    const bool softmax = p.score == KOSMOS_SCORE_SOFTMAX;
     if (!p.renorm) {
 #pragma unroll
-        for (int h = 0; h < N; ++h)
-            g[h] = !open[h] ? 0.f
-                            : p.scale * (p.score == KOSMOS_SCORE_SOFTMAX ? expf(x[h] - m) / z : 1.0f / (1.0f + expf(-x[h])));
+        for (int h = 0; h < N; ++h) {
+            const float e = expf(softmax ? x[h] - m : -x[h]);
+            g[h] = open[h] ? p.scale * (softmax ? __fdividef(e, z) : 1.0f / (1.0f + e)) : 0.f;
+        }
         return;
     }
     float top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int h = 0; h < N; ++h) top = fmaxf(top, open[h] ? x[h] : -INFINITY);
     top = row_max<L>(top);
-    if (p.score == KOSMOS_SCORE_SIGMOID) top = fminf(top, 0.f);
+    if (!softmax) top = fminf(top, 0.f);
 #pragma unroll
     for (int h = 0; h < N; ++h) {
-        g[h] = 0.f;
-        if (open[h]) {
-            if (p.score == KOSMOS_SCORE_SOFTMAX) g[h] = expf(x[h] - top);
-            else g[h] = x[h] > 0.f ? 1.0f / (1.0f + expf(-x[h])) : expf(x[h] - top) / (1.0f + expf(x[h]));
-        }
+        // sigmoid: e^x / (1 + e^x) for x <= 0, 1 / (1 + e^-x) above, relative to e^top
+        g[h] = expf((softmax ? x[h] : fminf(x[h], 0.f)) - top);
+        if (!softmax) g[h] = __fdividef(g[h], 1.0f + expf(-fabsf(x[h])));
+        if (!open[h]) g[h] = 0.f;
         sum += g[h];
     }
     sum = row_sum<L>(sum);
+    const float f = __fdividef(p.scale, sum);
 #pragma unroll
-    for (int h = 0; h < N; ++h) g[h] = open[h] ? p.scale * (g[h] / sum) : 0.f;
+    for (int h = 0; h < N; ++h) g[h] = open[h] ? g[h] * f : 0.f;
 }
 
 // ------------------------------------------------------------ fp32 choice
@@ -70,12 +81,12 @@ __device__ __forceinline__ void route_gates(const RouteParams &p, const float *x
 // than the scores' rounding error are chosen again in 64 bits.
 enum RouteMode : int { BY_LOGIT = 0, BY_SIGMOID = 1, BY_SOFTMAX = 2 };
 
-// Order-preserving map of floats to unsigned integers (-0 as +0).  Closed
+// Order-preserving map of floats to unsigned integers (-0 before +0).  Closed
 // experts have the key of -inf, and so have the places beyond E, which
 // come last of all because ties go to the lower expert.
 constexpr uint32_t KEY_NONE = 0u, KEY_CLOSED = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t float_key(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
+    const uint32_t b = __float_as_uint(x);
     return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_float(uint32_t k) {
@@ -106,23 +117,18 @@ __device__ __forceinline__ dd score_dd(bool softmax, float x, float b, float m, 
 __device__ __forceinline__ float difference(dd a, dd b) { return (a.hi - b.hi) + (a.lo - b.lo); }
 
 // A lane's best D keys in order.  A key's low bits hold the expert (as
-// MASK - e: the lower expert first), so keys differ and a maximum tells
+// mask - e: the lower expert first), so keys differ and a maximum tells
 // whose it is; a value's own low bits are lost, which matters to fp32 values
 // only (a bf16 or fp16 value has at least 13 zero bits).  A lane that has given
 // its list away makes the next one: of eight choices from eight lanes some lane
-// gives four in 13 rows of 100 and five in 2, from 32 lanes two in 60, four
-// in 0.2.
-template <int L, int V> struct Best {
-    static constexpr int D = L == 32 && V > 4 ? 3 : V > 8 ? 5 : 4;
-    static constexpr uint32_t MASK = L * V - 1;
+// gives four in 13 rows of 100 and five in 2.
+struct Best {
+    static constexpr int D = 5;
     uint32_t k[D];
-    // low: MASK - e for a lane's v = 0; the others' differ from it in v's bits alone
-    static __device__ __forceinline__ uint32_t key_of(float f, uint32_t low, uint32_t v_bits) {
-        return ((float_key(f) & ~MASK) | low) ^ v_bits;
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int d = 0; d < D; ++d) k[d] = KEY_NONE;
     }
-    static __device__ __forceinline__ uint32_t closed(uint32_t key) { return (key & MASK) | (KEY_CLOSED & ~MASK); }
-    static __device__ __forceinline__ int expert(uint32_t key) { return static_cast<int>(MASK - (key & MASK)); }
-    static __device__ __forceinline__ bool is_open(uint32_t key) { return (key | MASK) > KEY_CLOSED; }
     __device__ __forceinline__ void insert(uint32_t x) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -131,17 +137,10 @@ template <int L, int V> struct Best {
             k[d] = hi;
         }
     }
-    __device__ __forceinline__ void fill(const uint32_t *key) {
+    __device__ __forceinline__ void give() {
 #pragma unroll
-        for (int d = 0; d < D; ++d) k[d] = KEY_NONE;
-#pragma unroll
-        for (int v = 0; v < V; ++v) insert(key[v]);
-    }
-    __device__ __forceinline__ void fill_below(const uint32_t *key, uint32_t limit) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) k[d] = KEY_NONE;
-#pragma unroll
-        for (int v = 0; v < V; ++v) insert(key[v] < limit ? key[v] : KEY_NONE);
+        for (int d = 0; d + 1 < D; ++d) k[d] = k[d + 1];
+        k[D - 1] = KEY_NONE;
     }
 };
 
@@ -166,44 +165,36 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
 // scores, from the logits to the outputs.  fp64 instructions are slow here (two
 // lanes a cycle) and the row is waited for, so a score is computed in 64 bits only when
 // it comes up: until then its key is an upper bound, the fp32 score and its
-// error.  Lane l holds the experts l + 32 v.
-template <int VR> struct Row64 {
-    uint64_t key[VR];
-    float x[VR];
+// error.  Lane l holds the experts l + 32 v, their keys in shared memory.
+template <typename T> struct Row64 {
+    const RouteParams &p;
+    const T *row;
+    uint64_t *key;       // [E], shared
+    int lane;
     uint32_t exact = 0;  // one bit per value
     double m = 0.0, z = 1.0;
 
-    __device__ __forceinline__ double score(const RouteParams &p, float xv, int e) const {
-        const double d = xv;
-        const double q = p.score == KOSMOS_SCORE_SOFTMAX ? exp(d - m) / z : 1.0 / (1.0 + exp(-d));
-        return p.bias != nullptr ? q + static_cast<double>(p.bias[e]) : q;
-    }
-    // every lane makes one of its wanted values exact
-    __device__ __forceinline__ void sharpen(const RouteParams &p, int lane, uint32_t want) {
+    // every lane makes its wanted values exact
+    __device__ __forceinline__ void sharpen(uint32_t want) {
         while (__any_sync(FULL, want != 0u)) {
-            const int at = __ffs(want) - 1;
-            float xv = 0.f;
-#pragma unroll
-            for (int v = 0; v < VR; ++v)
-                if (v == at) xv = x[v];
-            const uint64_t k = at >= 0 ? double_key(score(p, xv, lane + 32 * at)) : 0;
-#pragma unroll
-            for (int v = 0; v < VR; ++v)
-                if (v == at) key[v] = k;
-            if (at >= 0) exact |= 1u << at;
-            want &= want - 1u;
+            if (want != 0u) {
+                const int at = __ffs(want) - 1, e = lane + 32 * at;
+                const double d = to_f32(row[e]);
+                double q = p.score == KOSMOS_SCORE_SOFTMAX ? exp(d - m) / z : 1.0 / (1.0 + exp(-d));
+                if (p.bias != nullptr) q += static_cast<double>(p.bias[e]);
+                key[e] = double_key(q);
+                exact |= 1u << at;
+                want &= want - 1u;
+            }
         }
     }
-    // the warp's best key among experts e0 <= e < e1 that are not in skip (one
-    // bit per value); its lane gets its place, the others -1
-    __device__ __forceinline__ uint64_t best(int lane, int e0, int e1, uint32_t skip, int &at) const {
+    // the warp's best key among experts e0 <= e < e1 whose bit is not in skip;
+    // its lane gets its place, the others -1
+    __device__ __forceinline__ uint64_t best(int e0, int e1, uint32_t skip, int &at) const {
         uint64_t k = 0;
         at = -1;
-#pragma unroll
-        for (int v = 0; v < VR; ++v) {
-            const int e = lane + 32 * v;
-            if (e >= e0 && e < e1 && !((skip >> v) & 1u) && key[v] > k) { k = key[v]; at = v; }
-        }
+        for (int v = 0, e = lane; e < e1; ++v, e += 32)
+            if (e >= e0 && !((skip >> v) & 1u) && key[e] > k) { k = key[e]; at = v; }
         const uint64_t b = warp_max_key(k);
         // ties: the lowest expert
         const uint32_t e = __reduce_min_sync(FULL, at >= 0 && k == b ? static_cast<uint32_t>(lane + 32 * at) : ~0u);
@@ -212,47 +203,44 @@ template <int VR> struct Row64 {
     }
 };
 
-template <typename T, int VR>
-__device__ __noinline__ void route_row_f64(const RouteParams &p, int64_t t, int lane, int32_t *s_hist) {
+template <typename T>
+__device__ __noinline__ void route_row_f64(const RouteParams &p, int64_t t, int lane, uint64_t *s_key, int32_t *s_hist) {
     const T *row = static_cast<const T *>(p.logits) + t * p.ld;
     const bool softmax = p.score == KOSMOS_SCORE_SOFTMAX, by_logit = p.bias == nullptr;
     const bool scores = !by_logit || (p.GK < p.G && p.group_top == 2);
-    Row64<VR> w;
+    Row64<T> w{p, row, s_key, lane};
     bool nan = false;
-    float top = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < VR; ++v) {
-        const int e = lane + 32 * v;
-        w.x[v] = e < p.E ? to_f32(row[e]) : -INFINITY;
-        nan = nan || w.x[v] != w.x[v] || (softmax && w.x[v] == INFINITY);
-        w.x[v] = fmaxf(w.x[v], -INFINITY);  // NaN: closed
-        top = fmaxf(top, w.x[v]);
+    float top = -INFINITY, rz = 1.f;
+    for (int e = lane; e < p.E; e += 32) {
+        const float x = to_f32(row[e]);
+        nan = nan || x != x || (softmax && x == INFINITY);
+        top = fmaxf(top, x);  // skips NaN
     }
     nan = __any_sync(FULL, nan);
-    float rz = 1.f;
     if (softmax && (scores || !p.renorm)) {
         top = row_max<32>(top);
         w.m = top;
         w.z = 0.0;
-#pragma unroll
-        for (int v = 0; v < VR; ++v)
-            if (w.x[v] > -INFINITY) w.z += exp(static_cast<double>(w.x[v]) - w.m);
+        for (int e = lane; e < p.E; e += 32) {
+            const float x = to_f32(row[e]);
+            if (x > -INFINITY) w.z += exp(static_cast<double>(x) - w.m);
+        }
         w.z = row_sum<32>(w.z);
         rz = static_cast<float>(1.0 / w.z);
     }
-#pragma unroll
-    for (int v = 0; v < VR; ++v) {
-        const int e = lane + 32 * v;
-        w.key[v] = KEY64_CLOSED;
-        if (w.x[v] > -INFINITY && scores) {
-            const float q = softmax ? fast_softmax(w.x[v], top, rz) : fast_sigmoid(w.x[v]);
+    for (int v = 0, e = lane; e < p.E; ++v, e += 32) {
+        const float x = to_f32(row[e]);
+        uint64_t k = KEY64_CLOSED;
+        if (x > -INFINITY && scores) {
+            const float q = softmax ? fast_softmax(x, top, rz) : fast_sigmoid(x);
             const float s = q + (by_logit ? 0.f : p.bias[e]);
-            if (s > -INFINITY) w.key[v] = double_key(static_cast<double>(s) + score_error(softmax, s, q, rz));
-        } else if (w.x[v] > -INFINITY) {
-            w.key[v] = double_key(static_cast<double>(w.x[v]));
+            if (s > -INFINITY) k = double_key(static_cast<double>(s) + score_error(softmax, s, q, rz));
+        } else if (x > -INFINITY) {
+            k = double_key(static_cast<double>(x));
         }
+        s_key[e] = k;
         // closed experts, infinite scores and logits are what they are
-        if (!scores || w.key[v] == KEY64_CLOSED || w.key[v] == double_key(INFINITY)) w.exact |= 1u << v;
+        if (!scores || k == KEY64_CLOSED || k == double_key(INFINITY)) w.exact |= 1u << v;
     }
     if (p.GK < p.G) {
         const int gs = p.E / p.G;
@@ -261,20 +249,21 @@ __device__ __noinline__ void route_row_f64(const RouteParams &p, int64_t t, int 
         while (again) {  // until every group's best group_top values are exact
             uint32_t want = 0u;
             for (int g = 0; g < p.G; ++g) {
-                int a1, a2 = -1;
-                const uint64_t b1 = w.best(lane, g * gs, (g + 1) * gs, 0u, a1);
-                double tt = key_double(b1);
-                if (p.group_top == 2) {
-                    const uint64_t b2 = w.best(lane, g * gs, (g + 1) * gs, a1 >= 0 ? 1u << a1 : 0u, a2);
-                    if (b2 > KEY64_CLOSED) tt += key_double(b2);
+                uint32_t mine = 0u;
+                double tt = 0.0;
+                for (int i = 0; i < p.group_top; ++i) {
+                    int at;
+                    const uint64_t b = w.best(g * gs, (g + 1) * gs, mine, at);
+                    if (at >= 0) mine |= 1u << at;
+                    if (i == 0) tt = key_double(b);
+                    else if (b > KEY64_CLOSED) tt += key_double(b);
                 }
                 if (lane == g) score = tt;
-                if (a1 >= 0) want |= 1u << a1;
-                if (a2 >= 0) want |= 1u << a2;
+                want |= mine;
             }
             want &= ~w.exact;
             again = __any_sync(FULL, want != 0u);
-            w.sharpen(p, lane, want);
+            w.sharpen(want);
         }
         int rank = 0;
         const uint64_t mine = double_key(score);
@@ -283,19 +272,15 @@ __device__ __noinline__ void route_row_f64(const RouteParams &p, int64_t t, int 
             rank += (o > mine || (o == mine && g < lane)) ? 1 : 0;
         }
         const uint32_t open = __ballot_sync(FULL, lane < p.G && rank < p.GK);
-#pragma unroll
-        for (int v = 0; v < VR; ++v) {
-            const int e = lane + 32 * v;
-            if (e < p.E && !((open >> (e / gs)) & 1u)) {
-                w.key[v] = KEY64_CLOSED;
+        for (int v = 0, e = lane; e < p.E; ++v, e += 32)
+            if (!((open >> (e / gs)) & 1u)) {
+                s_key[e] = KEY64_CLOSED;
                 w.exact |= 1u << v;
             }
-        }
     }
     if (by_logit && scores) {  // the scores were the groups'
-#pragma unroll
-        for (int v = 0; v < VR; ++v)
-            if (w.key[v] > KEY64_CLOSED) w.key[v] = double_key(static_cast<double>(w.x[v]));
+        for (int e = lane; e < p.E; e += 32)
+            if (s_key[e] > KEY64_CLOSED) s_key[e] = double_key(static_cast<double>(to_f32(row[e])));
         w.exact = ~0u;
     }
     int my_e = 0;
@@ -303,15 +288,14 @@ __device__ __noinline__ void route_row_f64(const RouteParams &p, int64_t t, int 
     uint32_t taken = 0u;
     for (int j = 0; j < p.k;) {
         int at;
-        const uint64_t b = w.best(lane, 0, p.E, taken, at);
+        const uint64_t b = w.best(0, p.E, taken, at);
         if (__any_sync(FULL, at >= 0 && !((w.exact >> at) & 1u))) {
             // an upper bound came up: every lane makes the best of its own that is left exact
             uint64_t k = 0;
             uint32_t want = 0u;
-#pragma unroll
-            for (int v = 0; v < VR; ++v)
-                if (!(((taken | w.exact) >> v) & 1u) && w.key[v] > k) { k = w.key[v]; want = 1u << v; }
-            w.sharpen(p, lane, want);
+            for (int v = 0, e = lane; e < p.E; ++v, e += 32)
+                if (!(((taken | w.exact) >> v) & 1u) && s_key[e] > k) { k = s_key[e]; want = 1u << v; }
+            w.sharpen(want);
             continue;
         }
         const int e = __reduce_max_sync(FULL, at >= 0 ? lane + 32 * at : 0);
@@ -330,20 +314,16 @@ __device__ __noinline__ void route_row_f64(const RouteParams &p, int64_t t, int 
         p.gate[t * p.k + lane] = g;
         if (p.counts != nullptr) atomicAdd(&s_hist[my_e], 1);
     }
+    __syncwarp();  // s_key is free again
 }
 
 // 1 / (sum of the row's exponentials) in double words, by the row's lanes.
-template <typename T, int L, int V>
-__device__ __noinline__ dd row_inverse_z(const T *row, int E, int l, bool vec, float m) {
-    float x[V];
-    Layout<T, L, V>::load(row, E, l, vec, x);
+template <typename T, int L>
+__device__ __noinline__ dd row_inverse_z(const T *row, int E, int l, float m) {
     dd z = {0.f, 0.f};
-#pragma unroll 1
-    for (int v = 0; v < V; ++v) {
-        const float xv = x[0];  // shifted down one by one: no indexed registers
-#pragma unroll
-        for (int i = 0; i + 1 < V; ++i) x[i] = x[i + 1];
-        if (xv > -INFINITY) z = dd_add(z, dd_exp(two_sum(xv, -m)));
+    for (int e0 = 0; e0 < E; e0 += L) {
+        const float x = e0 + l < E ? to_f32(row[e0 + l]) : -INFINITY;
+        if (x > -INFINITY) z = dd_add(z, dd_exp(two_sum(x, -m)));
     }
 #pragma unroll
     for (int d = L / 2; d > 0; d >>= 1) {
@@ -356,50 +336,42 @@ __device__ __noinline__ dd row_inverse_z(const T *row, int E, int l, bool vec, f
 }
 
 // ------------------------------------------------------------------ groups
-// The open groups of a warp's rows as bit masks.  The rows' values s (closed
-// experts -inf) pass through shared memory, where a lane takes every L-th group;
-// a group's stride there is four times an odd number, so that eight lanes'
-// 16-byte loads meet in no bank, and its padding holds -inf.  Where the values'
-// errors leave the border open, the groups' best values are looked up and the
-// scores taken again in double words; near then tells that those leave it open
-// too.
-template <typename T, int L, int V, int MODE>
-__device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *row, const float *s, float *s_row, int l,
-                                                int seg, float m, float rz, bool &near) {
-    using Lay = Layout<T, L, V>;
+// The open groups of a warp's rows as bit masks, from the rows' values in
+// shared memory (closed experts -inf).  A lane takes every L-th group; lanes begin at
+// different places of their groups, so that they do not meet in a bank.  Where
+// the values' errors leave the border open, the groups' best values are looked up
+// and the scores taken again in double words; near then tells that those
+// leave it open too.
+template <typename T, int L, int MODE>
+__device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *row, const float *s_row, int l, int seg,
+                                                float m, float rz, bool &near) {
     constexpr int NG = 32 / L;  // groups per lane
-    const bool fours = p.gs % 4 == 0;
-    __syncwarp();
-#pragma unroll
-    for (int v = 0; v < V; v += 4) {
-        const int e = Lay::expert(l, v);
-        if (fours) {
-            if (e < p.E)
-                *reinterpret_cast<float4 *>(s_row + e + ((e * p.gmul) >> 20) * (p.gsp - p.gs)) =
-                    make_float4(s[v], s[v + 1], s[v + 2], s[v + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (e + i < p.E) s_row[e + i + (((e + i) * p.gmul) >> 20) * (p.gsp - p.gs)] = s[v + i];
-        }
-    }
-    __syncwarp();
     const float err = MODE == BY_SOFTMAX ? 5.3e-6f * rz : 5e-7f;
     float sc[NG], ge[NG];
 #pragma unroll
     for (int h = 0; h < NG; ++h) {
         const int g = h * L + l;
         float t1 = -INFINITY, t2 = -INFINITY;
-        if (g < p.G)
-            for (int i = 0; i < p.gs; i += 4) {
-                const float4 q = *reinterpret_cast<const float4 *>(s_row + g * p.gsp + i);
-                const float qq[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    t2 = fmaxf(t2, fminf(t1, qq[j]));
-                    t1 = fmaxf(t1, qq[j]);
+        auto take = [&](float v) {
+            t2 = fmaxf(t2, fminf(t1, v));
+            t1 = fmaxf(t1, v);
+        };
+        if (h * L < p.G && g < p.G) {
+            if (p.gs % 4 == 0) {
+                const int n4 = p.gs / 4;
+                const float4 *q = reinterpret_cast<const float4 *>(s_row + g * p.gs);
+                int i = l % n4;
+#pragma unroll 1
+                for (int c = 0; c < n4; ++c) {
+                    const float4 f = q[i];
+                    take(f.x); take(f.y); take(f.z); take(f.w);
+                    if (++i == n4) i = 0;
                 }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < p.gs; ++i) take(s_row[g * p.gs + i]);
             }
+        }
         ge[h] = err + 2.4e-7f * fabsf(t1);  // a score's error and its part of the sum's
         if (p.group_top == 2 && t2 != -INFINITY) {
             ge[h] += err + 2.4e-7f * fabsf(t2);
@@ -416,6 +388,7 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *r
         int rank = 0;
 #pragma unroll
         for (int ho = 0; ho < NG; ++ho)
+#pragma unroll 1
             for (int o = 0; o < L && ho * L + o < p.G; ++o) {
                 const float v = __shfl_sync(FULL, sc[ho], seg * L + o);
                 rank += (v > sc[h] || (v == sc[h] && ho * L + o < g)) ? 1 : 0;
@@ -431,38 +404,50 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *r
     const bool open_border = hi != -INFINITY && !(lo > hi);
     if (!__any_sync(FULL, open_border)) return mask;
 
-    const dd drz = MODE == BY_SOFTMAX ? row_inverse_z<T, L, V>(row, p.E, l, p.vec, m) : dd{1.f, 0.f};
+    dd drz = {1.f, 0.f};
+    if (MODE == BY_SOFTMAX) drz = row_inverse_z<T, L>(row, p.E, l, m);
     bool bad = false;
     dd d[NG];
+    float gx[NG][2], gb[NG][2];  // the logits and biases behind a group's score
+    auto logit = [&](int e) { return to_f32(row[e]); };
+    auto bias = [&](int e) { return p.bias != nullptr ? p.bias[e] : 0.f; };
 #pragma unroll
     for (int h = 0; h < NG; ++h) {
         const int g = h * L + l;
         d[h] = {-INFINITY, 0.f};
+        gx[h][0] = gx[h][1] = gb[h][0] = gb[h][1] = 0.f;
         if (g >= p.G) continue;
         float t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
-        int e1 = 0, e2 = 0;
-        for (int i = 0; i < p.gs; ++i) {
-            const float v = s_row[g * p.gsp + i];
-            if (v > t1) { t3 = t2; t2 = t1; e2 = e1; t1 = v; e1 = i; }
-            else if (v > t2) { t3 = t2; t2 = v; e2 = i; }
-            else t3 = fmaxf(t3, v);
+        int e1 = 0, e2 = 0, e3 = 0;
+#pragma unroll 1
+        for (int i = g * p.gs; i < (g + 1) * p.gs; ++i) {
+            const float v = s_row[i];
+            if (v > t1) { t3 = t2; e3 = e2; t2 = t1; e2 = e1; t1 = v; e1 = i; }
+            else if (v > t2) { t3 = t2; e3 = e2; t2 = v; e2 = i; }
+            else if (v > t3) { t3 = v; e3 = i; }
         }
         if (t1 == -INFINITY) continue;
-        // the values left out have to be below those taken
-        const float next = p.group_top == 2 ? t3 : t2, least = p.group_top == 2 ? t2 : t1;
-        if (next > -INFINITY && !(least - next > 2.f * (err + 1.2e-7f * fabsf(least)) + 2.4e-7f * fabsf(next))) bad = true;
         if (!(fabsf(t1) < INFINITY)) bad = true;
-        e1 += g * p.gs;
-        e2 += g * p.gs;
-        d[h] = score_dd(MODE == BY_SOFTMAX, to_f32(row[e1]), p.bias != nullptr ? p.bias[e1] : 0.f, m, drz);
-        float de = score_error_dd(d[h].hi);
-        if (p.group_top == 2 && t2 > -INFINITY) {
-            const dd q = score_dd(MODE == BY_SOFTMAX, to_f32(row[e2]), p.bias != nullptr ? p.bias[e2] : 0.f, m, drz);
-            de += score_error_dd(q.hi);
-            d[h] = dd_add(d[h], q);
+        // the best value left out has to be below the last one taken, or the same
+        const float next = p.group_top == 2 ? t3 : t2, least = p.group_top == 2 ? t2 : t1;
+        const int en = p.group_top == 2 ? e3 : e2, el = p.group_top == 2 ? e2 : e1;
+        if (next > -INFINITY && !(least - next > 2.f * (err + 1.2e-7f * fabsf(least)) + 2.4e-7f * fabsf(next)) &&
+            !(logit(en) == logit(el) && bias(en) == bias(el)))
+            bad = true;
+        ge[h] = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < p.group_top; ++i) {
+            const int e = i == 0 ? e1 : e2;
+            if (i == 1 && t2 == -INFINITY) break;
+            const float x = logit(e), b = bias(e);
+            const dd q = score_dd(MODE == BY_SOFTMAX, x, b, m, drz);
+            ge[h] += score_error_dd(q.hi);
+            d[h] = i == 0 ? q : dd_add(d[h], q);
+            if (i == 0) { gx[h][0] = x; gb[h][0] = b; }
+            else { gx[h][1] = x; gb[h][1] = b; }
         }
-        ge[h] = de;
     }
+    __syncwarp();
     mask = 0u;
 #pragma unroll
     for (int h = 0; h < NG; ++h) {
@@ -471,20 +456,70 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *r
         int rank = 0;
 #pragma unroll
         for (int ho = 0; ho < NG; ++ho)
+#pragma unroll 1
             for (int o = 0; o < L && ho * L + o < p.G; ++o) {
-                const int src = seg * L + o;
+                const int src = seg * L + o, go = ho * L + o;
                 const dd v = {__shfl_sync(FULL, d[ho].hi, src), __shfl_sync(FULL, d[ho].lo, src)};
                 const float ve = __shfl_sync(FULL, ge[ho], src);
-                const int go = ho * L + o;
+                bool same = true;  // of the same logits and biases: a tie in 64 bits too
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    same = (__shfl_sync(FULL, gx[ho][i], src) == gx[h][i]) && same;
+                    same = (__shfl_sync(FULL, gb[ho][i], src) == gb[h][i]) && same;
+                }
                 const float by = difference(v, d[h]);  // NaN: neither has an open expert
                 rank += (by > 0.f || (!(by < 0.f) && go < g)) ? 1 : 0;
-                if (g < p.G && go != g && d[h].hi > -INFINITY && v.hi > -INFINITY && fabsf(by) <= ge[h] + ve) bad = true;
+                if (g < p.G && go != g && d[h].hi > -INFINITY && v.hi > -INFINITY && fabsf(by) <= ge[h] + ve && !same) bad = true;
             }
         mask |= (__ballot_sync(FULL, g < p.G && rank < p.GK) >> (seg * L) & row_lanes<L>()) << (h * L % 32);
     }
     const uint32_t bads = __ballot_sync(FULL, bad);  // by every lane: rows differ in open_border
     near = open_border && (bads >> (seg * L) & row_lanes<L>()) != 0u;
     return mask;
+}
+
+// A row's logits as floats to shared memory, PIECES loads of up to 16 bytes in
+// flight where the rows' places allow them.  Returns a sum that is 0 if they are
+// finite and NaN if not; want_m: m is the largest of
+// them (NaN apart).
+template <typename T, int L>
+__device__ __forceinline__ float stage_row(const T *row, int E, int l, bool vec, float *s_row, bool want_m, float &m) {
+    constexpr int W = 16 / static_cast<int>(sizeof(T)), PIECES = 4;
+    float odd = 0.f;
+    if (vec) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < E; c0 += PIECES * L * W) {
+            uint4 r[PIECES];
+#pragma unroll
+            for (int c = 0; c < PIECES; ++c) {
+                const int e = c0 + (c * L + l) * W;
+                r[c] = make_uint4(0, 0, 0, 0);
+                if (e < E) r[c] = *reinterpret_cast<const uint4 *>(row + e);
+            }
+#pragma unroll
+            for (int c = 0; c < PIECES; ++c) {
+                const int e = c0 + (c * L + l) * W;
+                if (e >= E) break;
+                const T *t = reinterpret_cast<const T *>(&r[c]);
+#pragma unroll
+                for (int i = 0; i < W; i += 4) {
+                    const float4 f = make_float4(to_f32(t[i]), to_f32(t[i + 1]), to_f32(t[i + 2]), to_f32(t[i + 3]));
+                    odd = fmaf(f.x, 0.f, fmaf(f.y, 0.f, fmaf(f.z, 0.f, fmaf(f.w, 0.f, odd))));
+                    if (want_m) m = fmaxf(fmaxf(m, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
+                    *reinterpret_cast<float4 *>(s_row + e + i) = f;
+                }
+            }
+        }
+    } else {
+#pragma unroll 8
+        for (int e = l; e < E; e += L) {
+            const float f = to_f32(row[e]);
+            odd = fmaf(f, 0.f, odd);
+            m = fmaxf(m, f);
+            s_row[e] = f;
+        }
+    }
+    return odd;
 }
 
 // A warp takes 32 / L consecutive rows at a time.  A row's lanes hold its
@@ -496,145 +531,189 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *r
 // would keep the loop's values out of registers.
 constexpr int LATER = 16;
 
-template <typename T, int L, int V, int MODE>
-__global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(const __grid_constant__ RouteParams p) {
+template <typename T, int L, int MODE>
+__global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(const __grid_constant__ RouteParams p) {
     constexpr bool EXACT = MODE == BY_LOGIT && sizeof(T) == 2;  // keys hold their values whole
     constexpr int R = 32 / L, N = L < SLOTS ? SLOTS / L : 1;    // rows of a warp, candidates of a lane
-    using Lay = Layout<T, L, V>;
-    using List = Best<L, V>;
-    constexpr uint32_t MASK = List::MASK, ROW = row_lanes<L>();
-    extern __shared__ int32_t s_mem[];
+    constexpr uint32_t ROW = row_lanes<L>();
+    extern __shared__ float s_mem[];
     __shared__ int64_t s_later[ROUTE_WARPS][LATER];
-    int32_t *s_hist = s_mem;                                           // [E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int seg = lane / L, l = lane % L;
-    float *s_row = reinterpret_cast<float *>(s_mem + p.hist_words) + (warp * R + seg) * p.row_words;
-    for (int i = threadIdx.x; i < p.hist_words; i += blockDim.x) s_hist[i] = 0;
-    if (p.GK < p.G)
-        for (int i = l; i < p.row_words; i += L) s_row[i] = -INFINITY;
-    __syncthreads();
+    // a row's values (p.width of them: E, rounded up to whole pieces of its lanes
+    // and filled with -inf), the bias, the counts
+    float *s_warp = s_mem + warp * p.warp_words, *s_row = s_warp + seg * p.width;
+    float *s_bias = s_mem + warps * p.warp_words;
+    int32_t *s_hist = reinterpret_cast<int32_t *>(s_bias + (MODE != BY_LOGIT ? p.width : 0));
+    if (p.counts != nullptr)
+        for (int i = threadIdx.x; i < p.E; i += blockDim.x) s_hist[i] = 0;
     pdl_wait();
+    if (MODE != BY_LOGIT)
+        for (int i = threadIdx.x; i < p.width; i += blockDim.x) {
+            const float b = i >= p.E ? -INFINITY : p.bias != nullptr ? p.bias[i] : 0.f;
+            s_bias[i] = fmaxf(b, -INFINITY);  // NaN: closed
+        }
+    __syncthreads();
     const bool softmax = MODE == BY_SOFTMAX || (MODE == BY_LOGIT && p.score == KOSMOS_SCORE_SOFTMAX);
     const bool need_z = MODE == BY_SOFTMAX || (softmax && !p.renorm);
+    const bool groups = p.GK < p.G;
+    const uint32_t mask = p.mask;  // a key's bits that hold the expert
     const T *logits = static_cast<const T *>(p.logits);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * warps * R;
     int64_t t0 = (static_cast<int64_t>(blockIdx.x) * warps + warp) * R;
     while (t0 < p.T) {
         int later = 0;
+        for (int e = p.E + l; e < p.width; e += L) s_row[e] = -INFINITY;
         for (; t0 < p.T && later <= LATER - R; t0 += stride) {
             const bool live = t0 + seg < p.T;
             const T *row = logits + (live ? t0 + seg : t0) * p.ld;
-            float s[V];
-            const float odd = Lay::load(row, p.E, l, p.vec, s);
             bool nan = false;
-            float m = 0.f, z = 1.f;
-            if (__any_sync(FULL, odd != 0.f)) {  // NaN or infinite logits
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    nan = nan || s[v] != s[v] || (softmax && s[v] == INFINITY);
-                    s[v] = fmaxf(s[v], -INFINITY);  // NaN: closed
+            float m = -INFINITY, z = 1.f, rz = 1.f;
+            __syncwarp();  // the row before is done with
+            const float odd = stage_row<T, L>(row, p.E, l, p.vec, s_row, need_z, m);
+            __syncwarp();
+            if (__any_sync(FULL, odd != 0.f)) {  // NaN or infinite logits; -inf needs nothing
+                bool fix = false;
+#pragma unroll 2
+                for (int e = 4 * l; e < p.width; e += 4 * L) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s_row + e);
+                    const bool nans = f.x != f.x || f.y != f.y || f.z != f.z || f.w != f.w;
+                    const bool infs = f.x == INFINITY || f.y == INFINITY || f.z == INFINITY || f.w == INFINITY;
+                    nan = nan || nans || (infs && softmax);
+                    fix = fix || nans || infs;
                 }
                 nan = (__ballot_sync(FULL, nan) >> (seg * L) & ROW) != 0u;
+                if (__any_sync(FULL, fix)) {
+#pragma unroll 1
+                    for (int e = l; e < p.E; e += L)
+                        // NaN: closed; the sigmoid's +inf as the largest number (its p is 1 too)
+                        s_row[e] = fminf(fmaxf(s_row[e], -INFINITY), MODE == BY_SIGMOID ? 3.402823466e38f : INFINITY);
+                    __syncwarp();
+                }
             }
-            if (softmax) {
-                m = s[0];
-#pragma unroll
-                for (int v = 1; v < V; ++v) m = fmaxf(m, s[v]);
-            }
-            // s: what orders the experts and scores the groups; closed experts -inf
-            float rz = 1.f;
             if (need_z) {
                 m = row_max<L>(m);
                 if (m == -INFINITY) m = 0.f;
                 z = 0.f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float q = ex2(LOG2E * (s[v] - m));
-                    z += q;
-                    if (MODE == BY_SOFTMAX) s[v] = s[v] > -INFINITY ? q : -INFINITY;
+#pragma unroll 2
+                for (int e = 4 * l; e < p.width; e += 4 * L) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s_row + e);
+                    z += (ex2(LOG2E * (f.x - m)) + ex2(LOG2E * (f.y - m))) + (ex2(LOG2E * (f.z - m)) + ex2(LOG2E * (f.w - m)));
                 }
                 z = row_sum<L>(z);
                 rz = rcp(z);
             }
-            uint32_t key[V];
-            const uint32_t low = MASK - Lay::expert(l, 0);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = Lay::expert(l, v);
+            // s: what orders the experts and scores the groups.  A closed expert's
+            // -inf turns x * 0 into a NaN, and the maximum the NaN into -inf.
+            auto score = [&](float x, float b) {
+                const float q = MODE == BY_SOFTMAX ? fast_softmax(x, m, rz) : fast_sigmoid(x);
+                return fmaxf(fmaf(x, 0.f, q + b), -INFINITY);
+            };
+            auto four = [&](int e) {
+                float4 f = *reinterpret_cast<const float4 *>(s_row + e);
                 if (MODE != BY_LOGIT) {
-                    const float b = p.bias != nullptr && e < p.E ? __ldg(p.bias + e) : 0.f;
-                    const float q = MODE == BY_SOFTMAX ? s[v] * rz : fast_sigmoid(s[v]);
-                    s[v] = s[v] > -INFINITY ? fmaxf(q + b, -INFINITY) : -INFINITY;
+                    const float4 b = *reinterpret_cast<const float4 *>(s_bias + e);
+                    f = make_float4(score(f.x, b.x), score(f.y, b.y), score(f.z, b.z), score(f.w, b.w));
                 }
-                key[v] = List::key_of(s[v], low, Lay::expert(0, v));
-            }
+                return f;
+            };
             bool near = false;
-            if (p.GK < p.G) {
-                const uint32_t open = open_groups<T, L, V, MODE>(p, row, s, s_row, l, seg, m, rz, near);
-                if (p.gs % 4 == 0) {  // four consecutive experts are of one group
-#pragma unroll
-                    for (int v = 0; v < V; v += 4)
-                        if (!((open >> (((Lay::expert(l, v) * p.gmul) >> 20) & 31)) & 1u)) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) key[v + i] = List::closed(key[v + i]);
-                        }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (!((open >> (((Lay::expert(l, v) * p.gmul) >> 20) & 31)) & 1u)) key[v] = List::closed(key[v]);
+            uint32_t open = FULL;
+            if (groups) {
+                if (MODE != BY_LOGIT) {
+#pragma unroll 2
+                    for (int e = 4 * l; e < p.width; e += 4 * L) *reinterpret_cast<float4 *>(s_row + e) = four(e);
+                    __syncwarp();
                 }
+                open = open_groups<T, L, MODE>(p, row, s_row, l, seg, m, rz, near);
             }
-            List list;
-            list.fill(key);
-            uint32_t my_key[N], best = KEY_NONE;
+            // ---- the rounds: lists (`list` from the keys below `limit`), then the
+            // largest of the lanes' best
+            Best list;
+            list.clear();
+            uint32_t my_key[N], best = ~0u;
 #pragma unroll
             for (int h = 0; h < N; ++h) my_key[h] = KEY_NONE;
-            auto next = [&](bool take) {  // the row's next key, if it takes one
-                const uint32_t b = row_max<L>(list.k[0]);
-                if (take) {
-                    best = b;
-                    if (list.k[0] == b) {
+            auto keys = [&](int e, uint32_t *key) {  // of four experts from e on
+                float4 f;
+                if (groups) f = *reinterpret_cast<const float4 *>(s_row + e);
+                else f = four(e);
+                const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                        for (int d = 0; d + 1 < List::D; ++d) list.k[d] = list.k[d + 1];
-                        list.k[List::D - 1] = KEY_NONE;
+                for (int i = 0; i < 4; ++i)  // a score is never -0, a logit may be
+                    key[i] = ((float_key(MODE == BY_LOGIT ? ff[i] + 0.f : ff[i]) & ~mask) | (mask - e)) ^ i;
+                if (groups) {
+                    if (p.gs % 4 == 0) {  // all of one group
+                        if (!((open >> (((e * p.gmul) >> 20) & 31)) & 1u)) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) key[i] = (key[i] & mask) | (KEY_CLOSED & ~mask);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((open >> ((((e + i) * p.gmul) >> 20) & 31)) & 1u)) key[i] = (key[i] & mask) | (KEY_CLOSED & ~mask);
                     }
                 }
-                if (List::D < V && __any_sync(FULL, list.k[0] == KEY_NONE)) {
-                    if (list.k[0] == KEY_NONE) list.fill_below(key, best);  // what is left of a row is below its best
+            };
+#pragma unroll LIST_UNROLL
+            for (int e = 4 * l; e < p.width; e += 4 * L) {
+                uint32_t key[4];
+                keys(e, key);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) list.insert(key[i]);
+            }
+            auto refill = [&]() {  // a lane without a list makes one of what is below its row's best so far
+                const uint32_t limit = list.k[0] == KEY_NONE ? best : 0u;
+#pragma unroll 1
+                for (int e = 4 * l; e < p.width; e += 4 * L) {
+                    uint32_t key[4];
+                    keys(e, key);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) list.insert(key[i] < limit ? key[i] : KEY_NONE);
                 }
             };
-            auto put = [&](int j) {
+            auto put = [&](int n) {
 #pragma unroll
                 for (int h = 0; h < N; ++h)
-                    if (j == h * L + l) my_key[h] = best;
+                    if (n == h * L + l) my_key[h] = best;
             };
+            int n = 0;  // candidates so far
 #pragma unroll 1
-            for (int j = 0; j < p.k; ++j) {
-                next(true);
-                put(j);
+            while (true) {
+                best = row_max<L>(list.k[0]);
+                if (list.k[0] == best) list.give();
+                put(n);
+                if (++n == p.k) break;
+                if (__any_sync(FULL, list.k[0] == KEY_NONE)) refill();
             }
-            int most = p.k;  // candidates of the longest row
             if (!EXACT && p.k < p.E) {
                 // the least key that may hide a score as large as the k-th's (its value is at
                 // least its key's): equal but for the expert, or within twice the error
-                uint32_t least = best & ~MASK;
+                uint32_t least = best & ~mask;
                 if (MODE != BY_LOGIT) {
                     const float sk = key_float(least);
-                    least = float_key(sk - 2.f * score_error(MODE == BY_SOFTMAX, sk, rz, rz)) & ~MASK;
+                    least = float_key(sk - 2.f * score_error(MODE == BY_SOFTMAX, sk, rz, rz) + 0.f) & ~mask;
                 }
-                const bool any_open = List::is_open(best);
-                next(true);
-                int n = p.k;
-                bool more = any_open && best >= least && List::is_open(best);
-                while (__any_sync(FULL, more && n < SLOTS && n + 1 < p.E)) {
-                    const bool take = more && n < SLOTS && n + 1 < p.E;
-                    if (take) put(n++);
-                    next(take);
-                    more = any_open && best >= least && List::is_open(best);
+                bool more = (best | mask) > KEY_CLOSED;
+                const int room = p.E < SLOTS + 1 ? p.E : SLOTS + 1;
+#pragma unroll 1
+                while (true) {
+                    if (__any_sync(FULL, more && list.k[0] == KEY_NONE)) refill();
+                    const uint32_t b = row_max<L>(list.k[0]);
+                    more = more && b >= least && (b | mask) > KEY_CLOSED;
+                    const bool take = more && n + 1 < room;
+                    near = near || (more && !take);  // no room for more candidates
+                    more = take;
+                    if (!__any_sync(FULL, take)) break;
+                    if (take) {
+                        best = b;
+                        if (list.k[0] == b) list.give();
+                        put(n);
+                    }
+                    ++n;
                 }
-                near = near || more;
-                most = __reduce_max_sync(FULL, n);
             }
+            const int used = n;  // candidates of the longest row
             // ---- candidates
             float my_x[N], my_g[N];
             int my_e[N], rank[N];
@@ -643,12 +722,12 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
             for (int h = 0; h < N; ++h) {
                 const bool mine = my_key[h] != KEY_NONE;
                 my_g[h] = 0.f;
-                my_open[h] = mine && List::is_open(my_key[h]);
-                my_e[h] = mine ? List::expert(my_key[h]) : 0;
+                my_open[h] = mine && (my_key[h] | mask) > KEY_CLOSED;
+                my_e[h] = mine ? static_cast<int>(mask - (my_key[h] & mask)) : 0;
                 rank[h] = mine ? h * L + l : p.k;
                 my_x[h] = 0.f;
-                if (h * L >= most) continue;
-                if (EXACT) my_x[h] = key_float((my_key[h] & 0x80000000u) ? my_key[h] & ~MASK : my_key[h] | MASK);
+                if (h * L >= used) continue;
+                if (EXACT) my_x[h] = key_float((my_key[h] & 0x80000000u) ? my_key[h] & ~mask : my_key[h] | mask);
                 else my_x[h] = to_f32(row[my_e[h]]);
             }
             if (!EXACT) {
@@ -660,7 +739,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
                 for (int h = 0; h < N; ++h) {
                     my_s[h] = -INFINITY;
                     my_b[h] = my_err[h] = 0.f;
-                    if (h * L >= most) continue;
+                    if (h * L >= used) continue;
                     my_b[h] = MODE != BY_LOGIT && p.bias != nullptr ? __ldg(p.bias + my_e[h]) : 0.f;
                     const float q = MODE == BY_SOFTMAX ? fast_softmax(my_x[h], m, rz) : fast_sigmoid(my_x[h]);
                     my_s[h] = !my_open[h] ? -INFINITY : MODE == BY_LOGIT ? my_x[h] : q + my_b[h];
@@ -668,11 +747,11 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
                 }
                 // in order already, as the keys are, unless some neighbours are not
                 // apart: compared with the next slot's score
-                bool apart = most <= L;
-                if (most <= L) {
+                bool apart = used <= L;
+                if (used <= L) {
                     const float s2 = __shfl_down_sync(FULL, my_s[0], 1);
                     const float err2 = MODE == BY_LOGIT ? 0.f : __shfl_down_sync(FULL, my_err[0], 1);
-                    apart = l >= most - 1 || l == L - 1 || s2 == -INFINITY || my_s[0] - s2 > my_err[0] + err2;
+                    apart = l >= used - 1 || l == L - 1 || s2 == -INFINITY || my_s[0] - s2 > my_err[0] + err2;
                 }
                 if (!__all_sync(FULL, apart)) {
 #pragma unroll
@@ -680,7 +759,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
                         if (my_key[h] != KEY_NONE) rank[h] = 0;
 #pragma unroll
                     for (int ho = 0; ho < N; ++ho)
-                        for (int o = 0; o < L && ho * L + o < most; ++o) {
+                        for (int o = 0; o < L && ho * L + o < used; ++o) {
                             const float so = __shfl_sync(FULL, my_s[ho], seg * L + o);
 #pragma unroll
                             for (int h = 0; h < N; ++h) {
@@ -693,7 +772,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
                         }
                 }
                 if (MODE != BY_LOGIT && __any_sync(FULL, close)) {
-                    const dd drz = MODE == BY_SOFTMAX ? row_inverse_z<T, L, V>(row, p.E, l, p.vec, m) : dd{1.f, 0.f};
+                    const dd drz = MODE == BY_SOFTMAX ? row_inverse_z<T, L>(row, p.E, l, m) : dd{1.f, 0.f};
                     dd my_d[N];
 #pragma unroll
                     for (int h = 0; h < N; ++h) {
@@ -706,7 +785,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
                     }
 #pragma unroll
                     for (int ho = 0; ho < N; ++ho)
-                        for (int o = 0; o < L && ho * L + o < most; ++o) {
+                        for (int o = 0; o < L && ho * L + o < used; ++o) {
                             const int src = seg * L + o;
                             const dd so = {__shfl_sync(FULL, my_d[ho].hi, src), __shfl_sync(FULL, my_d[ho].lo, src)};
                             const float xo = __shfl_sync(FULL, my_x[ho], src), bo = __shfl_sync(FULL, my_b[ho], src);
@@ -734,7 +813,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
             }
 #pragma unroll
             for (int h = 0; h < N; ++h) my_open[h] = my_open[h] && rank[h] < p.k;
-            if (N == 1 || most <= L) route_gates<L, 1>(p, my_x, my_open, m, z, my_g);
+            if (N == 1 || used <= L) route_gates<L, 1>(p, my_x, my_open, m, z, my_g);
             else route_gates<L, N>(p, my_x, my_open, m, z, my_g);
 #pragma unroll
             for (int h = 0; h < N; ++h)
@@ -746,7 +825,8 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
                 }
         }
         __syncwarp();
-        for (int i = 0; i < later; ++i) route_row_f64<T, (L * V) / 32>(p, s_later[warp][i], lane, s_hist);
+        for (int i = 0; i < later; ++i)
+            route_row_f64<T>(p, s_later[warp][i], lane, reinterpret_cast<uint64_t *>(s_warp), s_hist);
         __syncwarp();
     }
     pdl_trigger();
@@ -760,13 +840,11 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
     // the same sums); the last one hands them out and leaves zeros
     for (int i = threadIdx.x; i < p.E; i += blockDim.x)
         if (s_hist[i] != 0) atomicAdd(&p.acc[i], s_hist[i]);
-    __threadfence();
-    __syncthreads();
+    __syncthreads();  // the block's additions, and with them thread 0's release
     __shared__ int s_last;
-    if (threadIdx.x == 0) s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+    if (threadIdx.x == 0) s_last = atom_add_acqrel_gpu(p.ticket, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
     for (int i = threadIdx.x; i < p.E; i += blockDim.x) {
         p.counts[i] = __ldcg(&p.acc[i]);
         p.acc[i] = 0;
@@ -774,43 +852,36 @@ __global__ void __launch_bounds__(ROUTE_THREADS, route_blocks(V)) route_kernel(c
     if (threadIdx.x == 0) *p.ticket = 0u;
 }
 
-template <typename T, int L, int V, int MODE>
-kosmos_status launch_route_v(const RouteParams &q, int sms, cudaStream_t stream) {
+template <typename T, int L, int MODE>
+kosmos_status launch_route_l(const RouteParams &q, int sms, cudaStream_t stream) {
     RouteParams p = q;
-    constexpr int R = 32 / L, run = Layout<T, L, V>::W * sizeof(T);
-    p.vec = p.E % Layout<T, L, V>::W == 0 && reinterpret_cast<uintptr_t>(p.logits) % run == 0 &&
-            p.ld * static_cast<int64_t>(sizeof(T)) % run == 0;
-    p.hist_words = p.counts != nullptr ? static_cast<int>(align_up(p.E, 4)) : 0;
-    p.row_words = 0;
-    if (p.GK < p.G) {
-        p.gs = p.E / p.G;
-        p.gmul = ((1 << 20) + p.gs - 1) / p.gs;  // e * gmul >> 20 = e / gs for e < 1024
-        p.gsp = static_cast<int>(cdiv(p.gs, 4)) * 4;
-        if (p.gsp % 8 == 0) p.gsp += 4;
-        p.row_words = p.G * p.gsp;
-    }
+    constexpr int R = 32 / L, W = 16 / sizeof(T);
+    p.vec = p.E % W == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
+            p.ld * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+    p.width = static_cast<int>(align_up(p.E, 4 * L));
+    p.warp_words = p.width * (R > 2 ? R : 2);  // at least a row of 64-bit keys
+    p.mask = 31u;
+    while (p.mask < static_cast<uint32_t>(p.width - 1)) p.mask = 2 * p.mask + 1;
+    p.gs = p.E / p.G;
+    p.gmul = ((1 << 20) + p.gs - 1) / p.gs;  // e * gmul >> 20 = e / gs for e < 1024
+    const int shared_words = (MODE != BY_LOGIT ? p.width : 0) + (p.counts != nullptr ? p.E : 0);
     // few tokens: small blocks, over as many SMs as there are warps of rows
     int warps = ROUTE_WARPS;
     while (warps > 1 && cdiv(p.T, R * warps) < sms) warps /= 2;
-    // shared memory beyond 48 KB is not asked for: fewer warps per block instead
-    while (warps > 1 && 4ll * (p.hist_words + warps * R * p.row_words) > 40960) warps /= 2;
-    const size_t smem = 4ull * (p.hist_words + warps * R * p.row_words);
+    // at most 45 KB of shared memory: fewer warps per block beyond
+    while (warps > 1 && 4ll * (shared_words + warps * p.warp_words) > 46080) warps /= 2;
+    const size_t smem = 4ull * (shared_words + warps * p.warp_words);
     int64_t blocks = cdiv(p.T, R * warps);
-    const int64_t most = static_cast<int64_t>(route_blocks(V)) * (ROUTE_WARPS / warps) * sms;
+    const int64_t most = static_cast<int64_t>(ROUTE_BLOCKS) * (ROUTE_WARPS / warps) * sms;
     if (blocks > most) blocks = most;
-    return launch_overlapped(&route_kernel<T, L, V, MODE>, static_cast<unsigned>(blocks), warps * 32, smem, stream, p);
+    return launch_overlapped(&route_kernel<T, L, MODE>, static_cast<unsigned>(blocks), warps * 32, smem, stream, p);
 }
 
 template <typename T, int MODE> kosmos_status launch_route_m(const RouteParams &p, int sms, cudaStream_t stream) {
     // few tokens: a warp per row, whose latency counts
-    if (p.T <= SMALL_T * static_cast<int64_t>(sms) && p.E <= 256)
-        return p.E <= 128 ? launch_route_v<T, 32, 4, MODE>(p, sms, stream) : launch_route_v<T, 32, 8, MODE>(p, sms, stream);
-    if (p.E <= 32) return launch_route_v<T, 8, 4, MODE>(p, sms, stream);
-    if (p.E <= 64) return launch_route_v<T, 8, 8, MODE>(p, sms, stream);
-    if (p.E <= 128) return launch_route_v<T, 8, 16, MODE>(p, sms, stream);
-    if (p.E <= 256) return launch_route_v<T, 8, 32, MODE>(p, sms, stream);
-    if (p.E <= 512) return launch_route_v<T, 16, 32, MODE>(p, sms, stream);
-    return launch_route_v<T, 32, 32, MODE>(p, sms, stream);
+    if (p.T <= SMALL_T * static_cast<int64_t>(sms) || p.E > 512) return launch_route_l<T, 32, MODE>(p, sms, stream);
+    if (p.E <= 256) return launch_route_l<T, 8, MODE>(p, sms, stream);
+    return launch_route_l<T, 16, MODE>(p, sms, stream);
 }
 
 }  // namespace
