@@ -542,9 +542,11 @@ template <int N> kosmos_status launch_grad_n(const GradLaunch &L, int64_t chunk_
                 attr[0].val.cooperative = 1;
                 cfg.attrs = attr;
                 cfg.numAttrs = 1;
-                if (cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, p) == cudaSuccess) return KOSMOS_OK;
+                const cudaError_t e = cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, p);
+                if (e == cudaSuccess) return KOSMOS_OK;
                 (void)cudaGetLastError();
-                return KOSMOS_ERR_CUDA;
+                // fewer SMs than the device has are open to this process: two launches
+                if (e != cudaErrorCooperativeLaunchTooLarge) return KOSMOS_ERR_CUDA;
             }
             if (pass == 0 || chunks > 0) {
                 const kosmos_status st = launch_overlapped(pass == 0 ? &grad_norm_kernel<N> : &grad_scale_kernel<N>,

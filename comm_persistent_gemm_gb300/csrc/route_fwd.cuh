@@ -23,19 +23,23 @@ namespace {
 
 constexpr int ROUTE_WARPS = 8;
 constexpr int ROUTE_THREADS = ROUTE_WARPS * 32;
-#ifndef UN
-#define UN 2
-#endif
-#ifndef RB
-#define RB 5
-#endif
-constexpr int LIST_UNROLL = UN;
-constexpr int ROUTE_BLOCKS = RB;      // per SM, which the registers are made to fit
-#ifndef SMT
-#define SMT 20
-#endif
-constexpr int SMALL_T = SMT;         // tokens per SM up to which a warp takes one row
+constexpr int ROUTE_BLOCKS = 5;      // per SM, which the registers are made to fit
+// Tokens per SM up to which a warp takes one row: 2048 tokens of 128 / 256
+// experts take 5.3 / 8.9 us with one row a warp and 6.0 / 11.9 with four, 8192
+// tokens 8.9 / 16.9 and 6.3 / 14.7.
+constexpr int SMALL_T = 20;
 constexpr int SLOTS = 16;            // candidates that a row can have
+
+// Loops over a row in shared memory: a lane takes four values at 4 l, 4 (l + L),
+// ..., UNROLL of them at a time (a row's width is a multiple of that).
+template <int L> constexpr int UNROLL = L == 8 ? 2 : 1;
+template <int L, typename F> __device__ __forceinline__ void for_fours(int l, int width, F &&f) {
+#pragma unroll 1
+    for (int e = 4 * l; e < width; e += 4 * L * UNROLL<L>) {
+#pragma unroll
+        for (int u = 0; u < UNROLL<L>; ++u) f(e + u * 4 * L);
+    }
+}
 
 template <int L> constexpr uint32_t row_lanes() { return L == 32 ? FULL : (1u << L) - 1u; }
 
@@ -574,14 +578,13 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
             __syncwarp();
             if (__any_sync(FULL, odd != 0.f)) {  // NaN or infinite logits; -inf needs nothing
                 bool fix = false;
-#pragma unroll 2
-                for (int e = 4 * l; e < p.width; e += 4 * L) {
+                for_fours<L>(l, p.width, [&](int e) {
                     const float4 f = *reinterpret_cast<const float4 *>(s_row + e);
                     const bool nans = f.x != f.x || f.y != f.y || f.z != f.z || f.w != f.w;
                     const bool infs = f.x == INFINITY || f.y == INFINITY || f.z == INFINITY || f.w == INFINITY;
                     nan = nan || nans || (infs && softmax);
                     fix = fix || nans || infs;
-                }
+                });
                 nan = (__ballot_sync(FULL, nan) >> (seg * L) & ROW) != 0u;
                 if (__any_sync(FULL, fix)) {
 #pragma unroll 1
@@ -595,11 +598,10 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
                 m = row_max<L>(m);
                 if (m == -INFINITY) m = 0.f;
                 z = 0.f;
-#pragma unroll 2
-                for (int e = 4 * l; e < p.width; e += 4 * L) {
+                for_fours<L>(l, p.width, [&](int e) {
                     const float4 f = *reinterpret_cast<const float4 *>(s_row + e);
                     z += (ex2(LOG2E * (f.x - m)) + ex2(LOG2E * (f.y - m))) + (ex2(LOG2E * (f.z - m)) + ex2(LOG2E * (f.w - m)));
-                }
+                });
                 z = row_sum<L>(z);
                 rz = rcp(z);
             }
@@ -621,8 +623,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
             uint32_t open = FULL;
             if (groups) {
                 if (MODE != BY_LOGIT) {
-#pragma unroll 2
-                    for (int e = 4 * l; e < p.width; e += 4 * L) *reinterpret_cast<float4 *>(s_row + e) = four(e);
+                    for_fours<L>(l, p.width, [&](int e) { *reinterpret_cast<float4 *>(s_row + e) = four(e); });
                     __syncwarp();
                 }
                 open = open_groups<T, L, MODE>(p, row, s_row, l, seg, m, rz, near);
@@ -655,13 +656,12 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
                     }
                 }
             };
-#pragma unroll LIST_UNROLL
-            for (int e = 4 * l; e < p.width; e += 4 * L) {
+            for_fours<L>(l, p.width, [&](int e) {
                 uint32_t key[4];
                 keys(e, key);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) list.insert(key[i]);
-            }
+            });
             auto refill = [&]() {  // a lane without a list makes one of what is below its row's best so far
                 const uint32_t limit = list.k[0] == KEY_NONE ? best : 0u;
 #pragma unroll 1
@@ -858,7 +858,7 @@ kosmos_status launch_route_l(const RouteParams &q, int sms, cudaStream_t stream)
     constexpr int R = 32 / L, W = 16 / sizeof(T);
     p.vec = p.E % W == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
             p.ld * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-    p.width = static_cast<int>(align_up(p.E, 4 * L));
+    p.width = static_cast<int>(align_up(p.E, 4 * L * UNROLL<L>));
     p.warp_words = p.width * (R > 2 ? R : 2);  // at least a row of 64-bit keys
     p.mask = 31u;
     while (p.mask < static_cast<uint32_t>(p.width - 1)) p.mask = 2 * p.mask + 1;
