@@ -168,12 +168,24 @@ def opts(**kw) -> Opts:
     return o
 
 
+_current_stream = _current_device = None
+
+
+def _load_torch():
+    """torch's current-stream lookup, once a call needs it."""
+    global _current_stream, _current_device
+    import torch
+    torch.cuda.init()
+    _current_device = torch._C._cuda_getDevice
+    _current_stream = torch._C._cuda_getCurrentRawStream
+    return _current_stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
         # the current device's current stream without building a Stream
-        # object for it (0.3 instead of 3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # object for it (0.2 instead of 3 us a call)
+        return (_current_stream or _load_torch())(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -451,7 +463,8 @@ def _rows(what: str, t):
     and do not overlap."""
     if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{what}: a CUDA matrix expected")
-    (n, m), (ld, st) = t.shape, t.stride()
+    n, m = t.shape
+    ld, st = t.stride()
     if m > 1 and st != 1:
         raise ValueError(f"{what}: rows are not contiguous")
     if n <= 1:
