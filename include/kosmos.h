@@ -488,6 +488,7 @@ KOSMOS_API size_t kosmos_route_workspace_bytes(int n_experts);
  *   dgate         : [tokens, topk] fp32.
  *   dlogits       : out, [tokens, n_experts], the logits' type, rows ld_dlogits
  *                   elements apart; every element is written, rounded once.
+ *                   May be the logits themselves (the same stride).
  */
 KOSMOS_API kosmos_status kosmos_route_bwd(const void *logits, int dtype, int64_t tokens, int n_experts,
                                           int64_t ld_logits, const kosmos_router *router,
@@ -506,7 +507,7 @@ KOSMOS_API kosmos_status kosmos_route_bwd(const void *logits, int dtype, int64_t
  * Global norm: norm[0] = sqrt(sum over every tensor of x^2), and
  * tensor_norms[i] = the norm of tensor i alone (or NULL).  Squares are summed
  * in fp32 over at most 64 elements and from there in fp64, in an order that
- * depends on the sizes and the device alone (reruns are bit-identical); sums
+ * depends on the sizes and alignments alone (reruns are bit-identical); sums
  * that leave fp32's range are taken again in fp64, so that only a norm beyond
  * fp32 itself is inf.  NaN or inf anywhere gives NaN or inf.
  *   norm, tensor_norms : out, fp32 device memory.
@@ -525,6 +526,9 @@ KOSMOS_API kosmos_status kosmos_grad_norm(const void *const *grads, const int64_
  * place; nothing is written then when the factor is 1) or memory that overlaps
  * no tensor of the set.  A NaN norm gives NaN gradients, an infinite one
  * zeros (NaN where the gradient is infinite).  Finite max_norm >= 0.
+ * A small set (up to 16 KB for each of four blocks per SM) takes one
+ * cooperative launch whose blocks wait for one another; a wait that ran out
+ * (2 s) is KOSMOS_ERR_TIMEOUT in the workspace status, outputs then unwritten.
  */
 KOSMOS_API kosmos_status kosmos_grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
                                           const int32_t *dtypes, int n, float max_norm, float *norm, void *ws,
