@@ -205,7 +205,7 @@ template <typename T> kosmos_status launch_route_bwd_t(RouteBwdParams p, int sms
 
 }  // namespace
 
-size_t route_workspace_bytes(int E) { return 256 + static_cast<size_t>(align_up(4ll * E, 256)); }
+size_t route_workspace_bytes(int E) { return 256 + static_cast<size_t>(align_up(4ll * ROUTE_SUMS * E, 256)); }
 
 kosmos_status launch_route(const RouteLaunch &L, cudaStream_t stream) {
     if (L.T == 0) {

@@ -106,10 +106,12 @@ __device__ __forceinline__ float fast_softmax(float x, float m, float rz) { retu
 // which p (1 - p) brings under 6e-8; sum and reciprocal 3e-7 p; the bias'
 // addition 6e-8 |s|.  Softmax: e^-y of a term y below the maximum is off by
 // (2.5 + 1.7 y) steps, at most 3e-7 of the largest term; the row's sum and its
-// reciprocal by 5e-6 (its terms' errors weigh at most ln 1024, and there are
-// 37 additions); the bias as above.
+// reciprocal by 2.9e-6: its terms' errors, weighted by the terms, are at most
+// 2.5 + 1.7 ln 1024 steps (the weights' mean y is their entropy at most, less
+// ln z), a lane's sum and the lanes' take 15 roundings of half a step one after
+// another, the reciprocal and the product 1.5 steps; the bias as above.
 __device__ __forceinline__ float score_error(bool softmax, float s, float p, float rz) {
-    return (softmax ? 3e-7f * rz + 5e-6f * p : 5e-7f) + 1.2e-7f * fabsf(s);
+    return (softmax ? 3e-7f * rz + 2.9e-6f * p : 5e-7f) + 1.2e-7f * fabsf(s);
 }
 
 // The same for scores in double words.
@@ -133,13 +135,14 @@ struct Best {
 #pragma unroll
         for (int d = 0; d < D; ++d) k[d] = KEY_NONE;
     }
-    __device__ __forceinline__ void insert(uint32_t x) {
+    // two at a time, with three-way maxima: 14 instructions against 18 one by one
+    // (32768 rows of 256 bf16 values in 15.6 us against 16.4)
+    __device__ __forceinline__ void insert(uint32_t x, uint32_t y) {
+        const uint32_t a = max(x, y), b = min(x, y);
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const uint32_t hi = max(k[d], x);
-            x = min(k[d], x);
-            k[d] = hi;
-        }
+        for (int d = D - 1; d > 1; --d) k[d] = __vimax3_u32(k[d], min(k[d - 1], a), min(k[d - 2], b));
+        k[1] = __vimax3_u32(k[1], min(k[0], a), b);
+        k[0] = max(k[0], a);
     }
     __device__ __forceinline__ void give() {
 #pragma unroll
@@ -321,22 +324,35 @@ __device__ __noinline__ void route_row_f64(const RouteParams &p, int64_t t, int 
     __syncwarp();  // s_key is free again
 }
 
-// 1 / (sum of the row's exponentials) in double words, by the row's lanes.
+// 1 / (sum of the row's exponentials) in double words for the rows that have a
+// lane that wants it, one row after another by the whole warp: most often it
+// is one row of the warp's, and the warp waits for it.
 template <typename T, int L>
-__device__ __noinline__ dd row_inverse_z(const T *row, int E, int l, float m) {
-    dd z = {0.f, 0.f};
-    for (int e0 = 0; e0 < E; e0 += L) {
-        const float x = e0 + l < E ? to_f32(row[e0 + l]) : -INFINITY;
-        if (x > -INFINITY) z = dd_add(z, dd_exp(two_sum(x, -m)));
-    }
+__device__ __noinline__ dd row_inverse_z(const T *row, int E, int lane, float m, bool want) {
+    dd mine = {1.f, 0.f};
+    uint32_t todo = __ballot_sync(FULL, want);
+    while (todo != 0u) {
+        const int src = __ffs(todo) - 1, seg = src / L;
+        todo &= ~(row_lanes<L>() << (seg * L));
+        const T *r = reinterpret_cast<const T *>(__shfl_sync(FULL, reinterpret_cast<unsigned long long>(row), src));
+        const float rm = __shfl_sync(FULL, m, src);
+        dd z = {0.f, 0.f};
+        for (int e = lane; e < E; e += 32) {
+            const float x = to_f32(r[e]);
+            if (x > -INFINITY) z = dd_add(z, dd_exp(two_sum(x, -rm)));
+        }
+        __syncwarp();
 #pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) {
-        dd o;
-        o.hi = __shfl_xor_sync(FULL, z.hi, d);
-        o.lo = __shfl_xor_sync(FULL, z.lo, d);
-        z = dd_add(z, o);
+        for (int d = 16; d > 0; d >>= 1) {
+            dd o;
+            o.hi = __shfl_xor_sync(FULL, z.hi, d);
+            o.lo = __shfl_xor_sync(FULL, z.lo, d);
+            z = dd_add(z, o);
+        }
+        z = dd_inverse(z);
+        if (lane / L == seg) mine = z;
     }
-    return dd_inverse(z);
+    return mine;
 }
 
 // ------------------------------------------------------------------ groups
@@ -350,7 +366,7 @@ template <typename T, int L, int MODE>
 __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *row, const float *s_row, int l, int seg,
                                                 float m, float rz, bool &near) {
     constexpr int NG = 32 / L;  // groups per lane
-    const float err = MODE == BY_SOFTMAX ? 5.3e-6f * rz : 5e-7f;
+    const float err = MODE == BY_SOFTMAX ? 3.2e-6f * rz : 5e-7f;
     float sc[NG], ge[NG];
 #pragma unroll
     for (int h = 0; h < NG; ++h) {
@@ -409,7 +425,7 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *r
     if (!__any_sync(FULL, open_border)) return mask;
 
     dd drz = {1.f, 0.f};
-    if (MODE == BY_SOFTMAX) drz = row_inverse_z<T, L>(row, p.E, l, m);
+    if (MODE == BY_SOFTMAX) drz = row_inverse_z<T, L>(row, p.E, seg * L + l, m, open_border);
     bool bad = false;
     dd d[NG];
     float gx[NG][2], gb[NG][2];  // the logits and biases behind a group's score
@@ -452,7 +468,7 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *r
         }
     }
     __syncwarp();
-    mask = 0u;
+    uint32_t again = 0u;
 #pragma unroll
     for (int h = 0; h < NG; ++h) {
         if (h * L >= p.G) break;
@@ -475,11 +491,11 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *r
                 rank += (by > 0.f || (!(by < 0.f) && go < g)) ? 1 : 0;
                 if (g < p.G && go != g && d[h].hi > -INFINITY && v.hi > -INFINITY && fabsf(by) <= ge[h] + ve && !same) bad = true;
             }
-        mask |= (__ballot_sync(FULL, g < p.G && rank < p.GK) >> (seg * L) & row_lanes<L>()) << (h * L % 32);
+        again |= (__ballot_sync(FULL, g < p.G && rank < p.GK) >> (seg * L) & row_lanes<L>()) << (h * L % 32);
     }
     const uint32_t bads = __ballot_sync(FULL, bad);  // by every lane: rows differ in open_border
     near = open_border && (bads >> (seg * L) & row_lanes<L>()) != 0u;
-    return mask;
+    return open_border ? again : mask;
 }
 
 // A row's logits as floats to shared memory, PIECES loads of up to 16 bytes in
@@ -542,12 +558,14 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
     constexpr uint32_t ROW = row_lanes<L>();
     extern __shared__ float s_mem[];
     __shared__ int64_t s_later[ROUTE_WARPS][LATER];
+    __shared__ int16_t s_shift[ROUTE_WARPS][R][32];  // an open group's first expert less those of the open ones before it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int seg = lane / L, l = lane % L;
     // a row's values (p.width of them: E, rounded up to whole pieces of its lanes
     // and filled with -inf), the bias, the counts
     float *s_warp = s_mem + warp * p.warp_words, *s_row = s_warp + seg * p.width;
     float *s_bias = s_mem + warps * p.warp_words;
+    int16_t *s_open = s_shift[warp][seg];
     int32_t *s_hist = reinterpret_cast<int32_t *>(s_bias + (MODE != BY_LOGIT ? p.width : 0));
     if (p.counts != nullptr)
         for (int i = threadIdx.x; i < p.E; i += blockDim.x) s_hist[i] = 0;
@@ -576,21 +594,20 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
             __syncwarp();  // the row before is done with
             const float odd = stage_row<T, L>(row, p.E, l, p.vec, s_row, need_z, m);
             __syncwarp();
-            if (__any_sync(FULL, odd != 0.f)) {  // NaN or infinite logits; -inf needs nothing
+            const bool all_finite = __all_sync(FULL, odd == 0.f);
+            if (!all_finite) {  // NaN or infinite logits; -inf needs nothing
                 bool fix = false;
                 for_fours<L>(l, p.width, [&](int e) {
                     const float4 f = *reinterpret_cast<const float4 *>(s_row + e);
                     const bool nans = f.x != f.x || f.y != f.y || f.z != f.z || f.w != f.w;
                     const bool infs = f.x == INFINITY || f.y == INFINITY || f.z == INFINITY || f.w == INFINITY;
                     nan = nan || nans || (infs && softmax);
-                    fix = fix || nans || infs;
+                    fix = fix || nans;
                 });
                 nan = (__ballot_sync(FULL, nan) >> (seg * L) & ROW) != 0u;
                 if (__any_sync(FULL, fix)) {
 #pragma unroll 1
-                    for (int e = l; e < p.E; e += L)
-                        // NaN: closed; the sigmoid's +inf as the largest number (its p is 1 too)
-                        s_row[e] = fminf(fmaxf(s_row[e], -INFINITY), MODE == BY_SIGMOID ? 3.402823466e38f : INFINITY);
+                    for (int e = l; e < p.E; e += L) s_row[e] = fmaxf(s_row[e], -INFINITY);  // NaN: closed
                     __syncwarp();
                 }
             }
@@ -605,71 +622,75 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
                 z = row_sum<L>(z);
                 rz = rcp(z);
             }
-            // s: what orders the experts and scores the groups.  A closed expert's
+            // s: what orders the experts and scores the groups, in the logits' place.
+            // Where logits are not finite, a closed expert's has to be -inf: the
             // -inf turns x * 0 into a NaN, and the maximum the NaN into -inf.
-            auto score = [&](float x, float b) {
-                const float q = MODE == BY_SOFTMAX ? fast_softmax(x, m, rz) : fast_sigmoid(x);
-                return fmaxf(fmaf(x, 0.f, q + b), -INFINITY);
-            };
-            auto four = [&](int e) {
-                float4 f = *reinterpret_cast<const float4 *>(s_row + e);
-                if (MODE != BY_LOGIT) {
+            if (MODE != BY_LOGIT) {
+                auto scored = [&](int e, auto &&finish) {
+                    auto score = [&](float x, float b) {
+                        return finish(x, (MODE == BY_SOFTMAX ? fast_softmax(x, m, rz) : fast_sigmoid(x)) + b);
+                    };
+                    const float4 f = *reinterpret_cast<const float4 *>(s_row + e);
                     const float4 b = *reinterpret_cast<const float4 *>(s_bias + e);
-                    f = make_float4(score(f.x, b.x), score(f.y, b.y), score(f.z, b.z), score(f.w, b.w));
-                }
-                return f;
-            };
+                    *reinterpret_cast<float4 *>(s_row + e) =
+                        make_float4(score(f.x, b.x), score(f.y, b.y), score(f.z, b.z), score(f.w, b.w));
+                };
+                if (all_finite)
+                    for_fours<L>(l, p.width, [&](int e) { scored(e, [](float, float s) { return s; }); });
+                else
+                    for_fours<L>(l, p.width, [&](int e) {
+                        scored(e, [](float x, float s) { return fmaxf(fmaf(fminf(x, 0.f), 0.f, s), -INFINITY); });
+                    });
+                __syncwarp();
+            }
             bool near = false;
             uint32_t open = FULL;
-            if (groups) {
-                if (MODE != BY_LOGIT) {
-                    for_fours<L>(l, p.width, [&](int e) { *reinterpret_cast<float4 *>(s_row + e) = four(e); });
-                    __syncwarp();
-                }
-                open = open_groups<T, L, MODE>(p, row, s_row, l, seg, m, rz, near);
-            }
-            // ---- the rounds: lists (`list` from the keys below `limit`), then the
-            // largest of the lanes' best
+            if (groups) open = open_groups<T, L, MODE>(p, row, s_row, l, seg, m, rz, near);
+            // ---- the rounds: lists, then the largest of the lanes' best.  With groups
+            // only the open ones' experts are looked at, which a row of eight groups
+            // with four open has half of; `whole`: all of them, in a warp where fewer
+            // than k of those are open, so that closed experts are chosen too
             Best list;
             list.clear();
             uint32_t my_key[N], best = ~0u;
-#pragma unroll
-            for (int h = 0; h < N; ++h) my_key[h] = KEY_NONE;
+            int n = 0;  // candidates so far
             auto keys = [&](int e, uint32_t *key) {  // of four experts from e on
-                float4 f;
-                if (groups) f = *reinterpret_cast<const float4 *>(s_row + e);
-                else f = four(e);
+                const float4 f = *reinterpret_cast<const float4 *>(s_row + e);
                 const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)  // a score is never -0, a logit may be
                     key[i] = ((float_key(MODE == BY_LOGIT ? ff[i] + 0.f : ff[i]) & ~mask) | (mask - e)) ^ i;
-                if (groups) {
-                    if (p.gs % 4 == 0) {  // all of one group
-                        if (!((open >> (((e * p.gmul) >> 20) & 31)) & 1u)) {
+            };
+            auto close = [&](int e, uint32_t *key) {  // those of closed groups
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) key[i] = (key[i] & mask) | (KEY_CLOSED & ~mask);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (!((open >> ((((e + i) * p.gmul) >> 20) & 31)) & 1u)) key[i] = (key[i] & mask) | (KEY_CLOSED & ~mask);
-                    }
+                for (int i = 0; i < 4; ++i)
+                    if (!((open >> ((((e + i) * p.gmul) >> 20) & 31)) & 1u)) key[i] = (key[i] & mask) | (KEY_CLOSED & ~mask);
+            };
+            auto each_open = [&](auto &&f) {
+#pragma unroll 1
+                for (int q = 4 * l; q < p.GK * p.gs; q += 4 * L) {
+                    const int r = (q * p.gmul) >> 20;
+                    f(s_open[r] + q);
                 }
             };
-            for_fours<L>(l, p.width, [&](int e) {
-                uint32_t key[4];
-                keys(e, key);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) list.insert(key[i]);
-            });
+            bool whole = !groups || p.gs % 4 != 0;
             auto refill = [&]() {  // a lane without a list makes one of what is below its row's best so far
                 const uint32_t limit = list.k[0] == KEY_NONE ? best : 0u;
-#pragma unroll 1
-                for (int e = 4 * l; e < p.width; e += 4 * L) {
+                auto insert = [&](int e) {
                     uint32_t key[4];
                     keys(e, key);
+                    if (groups && whole) close(e, key);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) list.insert(key[i] < limit ? key[i] : KEY_NONE);
+                    for (int i = 0; i < 4; ++i)
+                        if (key[i] >= limit) key[i] = KEY_NONE;
+                    list.insert(key[0], key[1]);
+                    list.insert(key[2], key[3]);
+                };
+                if (whole) {
+#pragma unroll 1
+                    for (int e = 4 * l; e < p.width; e += 4 * L) insert(e);
+                } else {
+                    each_open(insert);
                 }
             };
             auto put = [&](int n) {
@@ -677,14 +698,40 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
                 for (int h = 0; h < N; ++h)
                     if (n == h * L + l) my_key[h] = best;
             };
-            int n = 0;  // candidates so far
+            if (!whole) {
+#pragma unroll
+                for (int h = 0; h < 32 / L; ++h) {
+                    const int g = h * L + l, r = __popc(open & ((1u << g) - 1u));
+                    if ((open >> g) & 1u) s_open[r] = static_cast<int16_t>((g - r) * p.gs);
+                }
+                __syncwarp();
+            }
 #pragma unroll 1
             while (true) {
-                best = row_max<L>(list.k[0]);
-                if (list.k[0] == best) list.give();
-                put(n);
-                if (++n == p.k) break;
-                if (__any_sync(FULL, list.k[0] == KEY_NONE)) refill();
+                list.clear();
+                best = ~0u;
+                n = 0;
+#pragma unroll
+                for (int h = 0; h < N; ++h) my_key[h] = KEY_NONE;
+                auto insert = [&](int e) {
+                    uint32_t key[4];
+                    keys(e, key);
+                    if (groups && whole) close(e, key);
+                    list.insert(key[0], key[1]);
+                    list.insert(key[2], key[3]);
+                };
+                if (whole) for_fours<L>(l, p.width, insert);
+                else each_open(insert);
+#pragma unroll 1
+                while (true) {
+                    best = row_max<L>(list.k[0]);
+                    if (list.k[0] == best) list.give();
+                    put(n);
+                    if (++n == p.k) break;
+                    if (__any_sync(FULL, list.k[0] == KEY_NONE)) refill();
+                }
+                if (whole || __all_sync(FULL, (best | mask) > KEY_CLOSED)) break;
+                whole = true;
             }
             if (!EXACT && p.k < p.E) {
                 // the least key that may hide a score as large as the k-th's (its value is at
@@ -772,16 +819,17 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
                         }
                 }
                 if (MODE != BY_LOGIT && __any_sync(FULL, close)) {
-                    const dd drz = MODE == BY_SOFTMAX ? row_inverse_z<T, L>(row, p.E, l, m) : dd{1.f, 0.f};
+                    const dd drz = MODE == BY_SOFTMAX ? row_inverse_z<T, L>(row, p.E, lane, m, close) : dd{1.f, 0.f};
+                    const bool row_close = (__ballot_sync(FULL, close) >> (seg * L) & ROW) != 0u;
                     dd my_d[N];
 #pragma unroll
                     for (int h = 0; h < N; ++h) {
                         my_d[h] = {-INFINITY, 0.f};
                         if (my_open[h]) {
                             if (fabsf(my_b[h]) < INFINITY) my_d[h] = score_dd(MODE == BY_SOFTMAX, my_x[h], my_b[h], m, drz);
-                            else near = true;
+                            else near = near || row_close;
                         }
-                        if (my_key[h] != KEY_NONE) rank[h] = 0;
+                        if (row_close && my_key[h] != KEY_NONE) rank[h] = 0;
                     }
 #pragma unroll
                     for (int ho = 0; ho < N; ++ho)
@@ -792,6 +840,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
 #pragma unroll
                             for (int h = 0; h < N; ++h) {
                                 const int me = h * L + l, it = ho * L + o;
+                                if (!row_close) continue;
                                 const float by = difference(so, my_d[h]);  // NaN: neither is open
                                 rank[h] += (by > 0.f || (!(by < 0.f) && it < me)) ? 1 : 0;
                                 // the same logit and bias are a tie in 64 bits too
@@ -838,16 +887,24 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
     }
     // blocks add their counts into the workspace (integers: any order gives
     // the same sums); the last one hands them out and leaves zeros
+    int32_t *acc = p.acc + blockIdx.x % ROUTE_SUMS * p.E;
     for (int i = threadIdx.x; i < p.E; i += blockDim.x)
-        if (s_hist[i] != 0) atomicAdd(&p.acc[i], s_hist[i]);
+        if (s_hist[i] != 0) atomicAdd(&acc[i], s_hist[i]);
     __syncthreads();  // the block's additions, and with them thread 0's release
     __shared__ int s_last;
     if (threadIdx.x == 0) s_last = atom_add_acqrel_gpu(p.ticket, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!s_last) return;
     for (int i = threadIdx.x; i < p.E; i += blockDim.x) {
-        p.counts[i] = __ldcg(&p.acc[i]);
-        p.acc[i] = 0;
+        int32_t c[ROUTE_SUMS], sum = 0;
+#pragma unroll
+        for (int b = 0; b < ROUTE_SUMS; ++b) c[b] = __ldcg(&p.acc[b * p.E + i]);
+#pragma unroll
+        for (int b = 0; b < ROUTE_SUMS; ++b) {
+            sum += c[b];
+            p.acc[b * p.E + i] = 0;
+        }
+        p.counts[i] = sum;
     }
     if (threadIdx.x == 0) *p.ticket = 0u;
 }
