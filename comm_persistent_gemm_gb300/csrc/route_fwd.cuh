@@ -25,8 +25,8 @@ constexpr int ROUTE_WARPS = 8;
 constexpr int ROUTE_THREADS = ROUTE_WARPS * 32;
 constexpr int ROUTE_BLOCKS = 5;      // per SM, which the registers are made to fit
 // Tokens per SM up to which a warp takes one row: 2048 tokens of 128 / 256
-// experts take 5.3 / 8.9 us with one row a warp and 6.0 / 11.9 with four, 8192
-// tokens 8.9 / 16.9 and 6.3 / 14.7.
+// experts take 4.9 / 8.3 us with one row a warp and 5.0 / 12.3 with four, 8192
+// tokens 8.0 / 15.5 and 6.3 / 12.8.
 constexpr int SMALL_T = 20;
 constexpr int SLOTS = 16;            // candidates that a row can have
 
@@ -922,10 +922,10 @@ kosmos_status launch_route_l(const RouteParams &q, int sms, cudaStream_t stream)
     p.gs = p.E / p.G;
     p.gmul = ((1 << 20) + p.gs - 1) / p.gs;  // e * gmul >> 20 = e / gs for e < 1024
     const int shared_words = (MODE != BY_LOGIT ? p.width : 0) + (p.counts != nullptr ? p.E : 0);
-    // few tokens: small blocks, over as many SMs as there are warps of rows
+    // Whole blocks for few tokens too: warps without a row help with the bias and
+    // the counts (16 x 256 in 5.8 us, with blocks of one warp on 16 SMs 9.8).
+    // At most 45 KB of shared memory: fewer warps per block beyond.
     int warps = ROUTE_WARPS;
-    while (warps > 1 && cdiv(p.T, R * warps) < sms) warps /= 2;
-    // at most 45 KB of shared memory: fewer warps per block beyond
     while (warps > 1 && 4ll * (shared_words + warps * p.warp_words) > 46080) warps /= 2;
     const size_t smem = 4ull * (shared_words + warps * p.warp_words);
     int64_t blocks = cdiv(p.T, R * warps);
