@@ -28,6 +28,10 @@ constexpr int ROUTE_BLOCKS = 5;      // per SM, which the registers are made to 
 // experts take 4.9 / 8.3 us with one row a warp and 5.0 / 12.3 with four, 8192
 // tokens 8.0 / 15.5 and 6.3 / 12.8.
 constexpr int SMALL_T = 20;
+// And up to which a warp takes two rows of up to 256 experts: 8192 tokens of
+// 256 / 128 experts take 12.4 / 6.3 us with two rows a warp and 14.2 / 6.3 with
+// four, 12288 tokens 16.5 / 8.2 and 16.2 / 7.2.
+constexpr int MEDIUM_T = 60;
 constexpr int SLOTS = 16;            // candidates that a row can have
 
 // Loops over a row in shared memory: a lane takes four values at 4 l, 4 (l + L),
@@ -439,12 +443,16 @@ __device__ __forceinline__ uint32_t open_groups(const RouteParams &p, const T *r
         if (g >= p.G) continue;
         float t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
         int e1 = 0, e2 = 0, e3 = 0;
-#pragma unroll 1
+#pragma unroll 4
         for (int i = g * p.gs; i < (g + 1) * p.gs; ++i) {
             const float v = s_row[i];
-            if (v > t1) { t3 = t2; e3 = e2; t2 = t1; e2 = e1; t1 = v; e1 = i; }
-            else if (v > t2) { t3 = t2; e3 = e2; t2 = v; e2 = i; }
-            else if (v > t3) { t3 = v; e3 = i; }
+            const bool first = v > t1, second = v > t2, third = v > t3;
+            t3 = second ? t2 : third ? v : t3;
+            e3 = second ? e2 : third ? i : e3;
+            t2 = first ? t1 : second ? v : t2;
+            e2 = first ? e1 : second ? i : e2;
+            t1 = first ? v : t1;
+            e1 = first ? i : e1;
         }
         if (t1 == -INFINITY) continue;
         if (!(fabsf(t1) < INFINITY)) bad = true;
@@ -807,14 +815,22 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
 #pragma unroll
                     for (int ho = 0; ho < N; ++ho)
                         for (int o = 0; o < L && ho * L + o < used; ++o) {
-                            const float so = __shfl_sync(FULL, my_s[ho], seg * L + o);
+                            const int src = seg * L + o;
+                            const float so = __shfl_sync(FULL, my_s[ho], src);
+                            float xo = 0.f, bo = 0.f;
+                            if (MODE != BY_LOGIT) {
+                                xo = __shfl_sync(FULL, my_x[ho], src);
+                                bo = __shfl_sync(FULL, my_b[ho], src);
+                            }
 #pragma unroll
                             for (int h = 0; h < N; ++h) {
                                 const int me = h * L + l, it = ho * L + o;
-                                rank[h] += (so > my_s[h] || (so == my_s[h] && it < me)) ? 1 : 0;
+                                // the same logit and bias are a tie in 64 bits too
+                                const bool tie = MODE != BY_LOGIT && xo == my_x[h] && bo == my_b[h];
+                                rank[h] += (so > my_s[h] || ((so == my_s[h] || tie) && it < me)) ? 1 : 0;
                                 // a pair within its errors: the wider one's is at least half of their sum
                                 if (MODE != BY_LOGIT)
-                                    close = close || (it != me && fabsf(so - my_s[h]) <= 2.f * my_err[h]);
+                                    close = close || (!tie && fabsf(so - my_s[h]) <= 2.f * my_err[h]);
                             }
                         }
                 }
@@ -937,7 +953,7 @@ kosmos_status launch_route_l(const RouteParams &q, int sms, cudaStream_t stream)
 template <typename T, int MODE> kosmos_status launch_route_m(const RouteParams &p, int sms, cudaStream_t stream) {
     // few tokens: a warp per row, whose latency counts
     if (p.T <= SMALL_T * static_cast<int64_t>(sms) || p.E > 512) return launch_route_l<T, 32, MODE>(p, sms, stream);
-    if (p.E <= 256) return launch_route_l<T, 8, MODE>(p, sms, stream);
+    if (p.E <= 256 && p.T > MEDIUM_T * static_cast<int64_t>(sms)) return launch_route_l<T, 8, MODE>(p, sms, stream);
     return launch_route_l<T, 16, MODE>(p, sms, stream);
 }
 
