@@ -66,8 +66,9 @@ KOS_HD dd dd_exp(dd y) {
     constexpr float LOG2E_F = 1.4426950408889634f;
     // ln 2 in three parts: 16 bits (a multiple of it by n is exact), 24 bits, the rest
     constexpr float LN2_1 = 45426.0f / 65536.0f, LN2_2 = 0x1.7f7d1cp-20f, LN2_3 = 5.497923e-14f;
-    const float n = rintf(mul_rn(y.hi, LOG2E_F));
-    if (!(n >= -120.0f)) return {0.0f, 0.0f};
+    float n = rintf(mul_rn(y.hi, LOG2E_F));
+    const bool zero = !(n >= -120.0f);  // no branch: several exponentials run side by side
+    if (zero) n = y.hi = y.lo = 0.0f;
     const float r1 = fmaf(-n, LN2_1, y.hi);
     const float p = mul_rn(n, LN2_2);
     dd r = two_sum(r1, -p);
@@ -89,7 +90,7 @@ KOS_HD dd dd_exp(dd y) {
 #else
     const float scale = ldexpf(1.0f, static_cast<int>(n));
 #endif
-    return {e.hi * scale, e.lo * scale};
+    return {zero ? 0.0f : e.hi * scale, zero ? 0.0f : e.lo * scale};
 }
 
 // 1 / (1 + e^-x), off by at most 2e-11.

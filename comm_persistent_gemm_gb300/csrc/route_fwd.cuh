@@ -341,10 +341,8 @@ __device__ __noinline__ dd row_inverse_z(const T *row, int E, int lane, float m,
         const T *r = reinterpret_cast<const T *>(__shfl_sync(FULL, reinterpret_cast<unsigned long long>(row), src));
         const float rm = __shfl_sync(FULL, m, src);
         dd z = {0.f, 0.f};
-        for (int e = lane; e < E; e += 32) {
-            const float x = to_f32(r[e]);
-            if (x > -INFINITY) z = dd_add(z, dd_exp(two_sum(x, -rm)));
-        }
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) z = dd_add(z, dd_exp(two_sum(to_f32(r[e]), -rm)));  // NaN, -inf: 0
         __syncwarp();
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
