@@ -5,7 +5,7 @@
 // translation unit per type of logits instantiates it.
 //
 // L lanes of a warp share a row (8 up to 256 experts, so that a warp orders
-// four rows at once); its values wait in shared memory.  The choice is k rounds of
+// four rows at once; 4 for few experts and choices); its values wait in shared memory.  The choice is k rounds of
 // a maximum over the lanes; what decides it is an order in which ties go to
 // the lower expert, so the result is a function of the row alone.
 //
@@ -32,11 +32,19 @@ constexpr int SMALL_T = 20;
 // 256 / 128 experts take 12.4 / 6.3 us with two rows a warp and 14.2 / 6.3 with
 // four, 12288 tokens 16.5 / 8.2 and 16.2 / 7.2.
 constexpr int MEDIUM_T = 60;
-constexpr int SLOTS = 16;            // candidates that a row can have
+// And from which a warp takes eight rows of up to 64 experts (of up to 128 from
+// twice as many on), without groups and of so few choices that four lanes'
+// lists do not run out: 262144 tokens of 60 fp16 experts, top-4, take 38 us
+// with eight rows a warp and 52 with four, of 8 experts, top-2, 23 and 41, of
+// 128, 50 and 59; 12288 tokens of 60 bf16 experts with a bias 9.1 and 8.4,
+// 19000 of 128 10.9 and 10.3; top-8 of 128, 262144 tokens, 71 and 68.
+constexpr int MANY_T = 120;
+constexpr int FEW_TOPK = 4;
+constexpr int SLOTS = 16;            // candidates that a row can have (8 where four lanes share it)
 
 // Loops over a row in shared memory: a lane takes four values at 4 l, 4 (l + L),
 // ..., UNROLL of them at a time (a row's width is a multiple of that).
-template <int L> constexpr int UNROLL = L == 8 ? 2 : 1;
+template <int L> constexpr int UNROLL = L <= 8 ? 2 : 1;
 template <int L, typename F> __device__ __forceinline__ void for_fours(int l, int width, F &&f) {
 #pragma unroll 1
     for (int e = 4 * l; e < width; e += 4 * L * UNROLL<L>) {
@@ -560,7 +568,8 @@ constexpr int LATER = 16;
 template <typename T, int L, int MODE>
 __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(const __grid_constant__ RouteParams p) {
     constexpr bool EXACT = MODE == BY_LOGIT && sizeof(T) == 2;  // keys hold their values whole
-    constexpr int R = 32 / L, N = L < SLOTS ? SLOTS / L : 1;    // rows of a warp, candidates of a lane
+    constexpr int ROOM = L == 4 ? 8 : SLOTS;
+    constexpr int R = 32 / L, N = L < ROOM ? ROOM / L : 1;      // rows of a warp, candidates of a lane
     constexpr uint32_t ROW = row_lanes<L>();
     extern __shared__ float s_mem[];
     __shared__ int64_t s_later[ROUTE_WARPS][LATER];
@@ -584,7 +593,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
     __syncthreads();
     const bool softmax = MODE == BY_SOFTMAX || (MODE == BY_LOGIT && p.score == KOSMOS_SCORE_SOFTMAX);
     const bool need_z = MODE == BY_SOFTMAX || (softmax && !p.renorm);
-    const bool groups = p.GK < p.G;
+    const bool groups = L > 4 && p.GK < p.G;
     const uint32_t mask = p.mask;  // a key's bits that hold the expert
     const T *logits = static_cast<const T *>(p.logits);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * warps * R;
@@ -748,7 +757,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, ROUTE_BLOCKS) route_kernel(cons
                     least = float_key(sk - 2.f * score_error(MODE == BY_SOFTMAX, sk, rz, rz) + 0.f) & ~mask;
                 }
                 bool more = (best | mask) > KEY_CLOSED;
-                const int room = p.E < SLOTS + 1 ? p.E : SLOTS + 1;
+                const int room = p.E < ROOM + 1 ? p.E : ROOM + 1;
 #pragma unroll 1
                 while (true) {
                     if (__any_sync(FULL, more && list.k[0] == KEY_NONE)) refill();
@@ -951,6 +960,8 @@ kosmos_status launch_route_l(const RouteParams &q, int sms, cudaStream_t stream)
 template <typename T, int MODE> kosmos_status launch_route_m(const RouteParams &p, int sms, cudaStream_t stream) {
     // few tokens: a warp per row, whose latency counts
     if (p.T <= SMALL_T * static_cast<int64_t>(sms) || p.E > 512) return launch_route_l<T, 32, MODE>(p, sms, stream);
+    if (p.E <= 128 && p.k <= FEW_TOPK && p.GK == p.G && p.T > (p.E <= 64 ? MANY_T : 2 * MANY_T) * static_cast<int64_t>(sms))
+        return launch_route_l<T, 4, MODE>(p, sms, stream);
     if (p.E <= 256 && p.T > MEDIUM_T * static_cast<int64_t>(sms)) return launch_route_l<T, 8, MODE>(p, sms, stream);
     return launch_route_l<T, 16, MODE>(p, sms, stream);
 }

@@ -232,6 +232,64 @@ def test_biases_next_to_one_another(K, score, bits):
         check_route(K, x.cuda(), {"topk": k, "score": score, **kw}, bias.cuda())
 
 
+# T, E, topk, groups: so many tokens that a warp takes two, four, eight rows at once
+SHARED = [
+    (4001, 256, 8, (8, 4, 2)),
+    (7003, 40, 16, (1, 1, 1)),
+    (10007, 256, 8, (8, 4, 2)),
+    (10007, 128, 6, (16, 3, 1)),
+    (10007, 60, 8, (1, 1, 1)),
+    (12001, 500, 10, (1, 1, 1)),
+    (20011, 60, 4, (1, 1, 1)),
+    (20011, 8, 2, (1, 1, 1)),
+    (20011, 3, 3, (1, 1, 1)),
+    (20011, 1, 1, (1, 1, 1)),
+    (40009, 100, 4, (1, 1, 1)),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("has_bias", [False, True])
+@pytest.mark.parametrize("i", range(len(SHARED)))
+def test_rows_that_share_a_warp(K, i, has_bias, score, dtype):
+    """Ordinary rows next to masked ones, ties, scores that differ by 2^-30 and
+    (compared with the run without them) rows with NaN: each is decided as if
+    it were alone.  Groups scored by sums have no rows of ties under a bias:
+    whether such sums are equal would depend on their roundings in 64 bits."""
+    T, E, k, (n_groups, topk_groups, group_top) = SHARED[i]
+    g = torch.Generator().manual_seed(200 + i)
+    x = torch.randn(T, E, generator=g)
+    t = torch.arange(T)
+    if group_top == 1 or not has_bias:
+        x[t % 11 == 1] = 0.0
+    if n_groups == 1:
+        x[t % 11 == 3] = torch.randint(0, 3, (int((t % 11 == 3).sum()), E), generator=g).float() * 0.5
+    few = torch.rand(T, E, generator=g) < 0.02
+    x[(t % 11 == 5)[:, None] & ~few] = -math.inf                                  # a few open, or none
+    x[(t % 11 == 6)[:, None] & few] = -math.inf
+    x[t % 997 == 7] = -math.inf
+    x = x.to(DT[dtype])
+    bias = None
+    if has_bias:
+        bias = torch.randint(-20, 21, (E,), generator=g).float() * 2.0 ** -30
+        if E > 4:
+            bias[E // 2] = -math.inf
+        bias = bias.cuda()
+    c = {"topk": k, "score": score, "n_groups": n_groups, "topk_groups": topk_groups, "group_top": group_top,
+         "scale": 1.5}
+    check_route(K, x.cuda(), c, bias)
+    c["renorm"] = False
+    gi, gate, _ = check_route(K, x.cuda(), c, bias)
+    bad = (t % 101 == 50) & (t % 11 != 5)
+    x[bad, E // 3] = math.nan
+    idx, gate_nan, _ = run_route(K, x.cuda(), c, bias)
+    keep = ~bad
+    assert torch.equal(idx.cpu().long()[keep], gi[keep])
+    assert torch.equal(gate_nan.cpu()[keep], gate.cpu()[keep])
+    assert bool(torch.isnan(gate_nan.cpu()[bad]).all())
+
+
 def test_nan_and_infinite_logits(K):
     for score in ("softmax", "sigmoid"):
         for dtype in (torch.float32, torch.bfloat16):
