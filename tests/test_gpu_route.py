@@ -248,6 +248,31 @@ SHARED = [
 ]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,E,k,pad", [(37, 8, 2, 0), (501, 16, 9, 3), (2003, 31, 16, 0), (160003, 8, 2, 0),
+                                       (160003, 57, 6, 1)])
+def test_gradient_of_gates_that_are_not_renormalised(K, T, E, k, pad, dtype):
+    """Few experts, where many rows share a warp, with masked rows among them."""
+    g = torch.Generator().manual_seed(T + E)
+    wide = torch.randn(T, E + pad, generator=g)
+    wide[::13, : E - 1] = -math.inf
+    wide[::29] = -math.inf
+    logits = wide.to(DT[dtype]).cuda()[:, :E]
+    x = logits.float().cpu()
+    c = {"topk": k, "score": "softmax", "renorm": False, "scale": 0.75}
+    gi, gate, is_open = check_route(K, logits, c)
+    dgate = torch.randn(T, k, generator=g)
+    out = torch.full((T, E + pad), 7.0, dtype=logits.dtype, device="cuda")
+    K.route_bwd(logits, make_router(K, c), gi.int().cuda(), gate, dgate.cuda(), out[:, :E])
+    assert bool((out[:, E:] == 7.0).all())
+    dl, mag = route_bwd_ref(x, gi, is_open, dgate, score="softmax", renorm=False, scale=0.75)
+    tol = 2 * (32 + E / 32 + 2 * row_range(x)) * U
+    lim = tol * mag + torch.finfo(logits.dtype).eps / 2 * dl.abs() * (1 + 2 ** -6) + \
+        (2.0 ** -25 if logits.dtype == torch.float16 else 1e-38)
+    err = (out[:, :E].cpu().double() - dl).abs()
+    assert bool((err <= lim).all()), float((err - lim).max())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("has_bias", [False, True])
