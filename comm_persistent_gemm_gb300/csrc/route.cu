@@ -98,13 +98,17 @@ __global__ void __launch_bounds__(BWD_THREADS) route_bwd_chosen_kernel(const __g
     }
 }
 
+// Blocks per SM that the registers are made to fit: 500009 x 256 fp32 take 179 us
+// with four and 201 with three, 1000003 x 128 194 us with five and 214 with four.
+template <int V> constexpr int BWD_BLOCKS = V <= 16 ? 5 : 4;
+
 // The softmax without renorm: every expert of a row has the gradient -p D, the
 // chosen ones g dg besides.  L lanes share a row, as in the forward, its values
 // in registers.  262144 x 60 fp16 in rows of 65: 21.9 us, bound by instruction
 // issue (2-byte loads, and stores to shared memory); wide rows by memory:
-// 1000003 x 128 fp32 in 214 us, 4.8 TB/s.
+// 500009 x 128 fp32 in 101 us, 5.1 TB/s.
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(BWD_THREADS) route_bwd_all_kernel(const __grid_constant__ RouteBwdParams p) {
+__global__ void __launch_bounds__(BWD_THREADS, BWD_BLOCKS<V>) route_bwd_all_kernel(const __grid_constant__ RouteBwdParams p) {
     using Lay = Layout<T, L, V>;
     constexpr int R = 32 / L, N = L < KOSMOS_ROUTE_MAX_TOPK ? KOSMOS_ROUTE_MAX_TOPK / L : 1;
     extern __shared__ uint4 s_mem[];
@@ -178,7 +182,7 @@ template <typename T, int L, int V> kosmos_status launch_bwd_all(RouteBwdParams 
     int warps = BWD_WARPS;
     while (warps > 1 && cdiv(p.T, R * warps) < sms) warps /= 2;
     int64_t blocks = cdiv(p.T, R * warps);
-    const int64_t most = 4ll * (BWD_WARPS / warps) * sms;
+    const int64_t most = static_cast<int64_t>(BWD_BLOCKS<V>) * (BWD_WARPS / warps) * sms;
     if (blocks > most) blocks = most;
     return launch_overlapped(&route_bwd_all_kernel<T, L, V>, static_cast<unsigned>(blocks), warps * 32, warps * p.tile, stream,
                              p);
